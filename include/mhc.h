@@ -18,7 +18,8 @@
  *     there and keeps them until the process exits.)
  *   - Arguments are validated on the host before anything is launched; a negative return code
  *     means nothing was launched (except MHC_ERR_CUDA, which reports a launch failure).
- *   - Only n = 4 streams is built (the shape of the pages' block; (2+n)n = 24 mix numbers).
+ *   - Only n = 4 streams is built (the shape of the pages' block; (2+n)n = 24 mix numbers), except
+ *     for the norm step, which also takes n = 1.
  */
 #ifndef MHC_H
 #define MHC_H
@@ -85,6 +86,11 @@ extern "C" {
  *   mhc_fused_step_mxfp8). The cluster kernel ignores the step scratch.                      */
 #define MHC_PATH_PERSISTENT      0x8u
 #define MHC_PATH_CLUSTER         0x10u
+/* Norm step only (mhc_norm_step and its backward; MHC_ERR_SHAPE there for any other flag but
+ * MHC_COMB_ROW_DEST). MHC_GATE_SIGMOID: the gate tensor holds logits, the gate is their sigmoid.
+ * MHC_WEIGHTS_SHARED: pre, post and comb (and their gradients) hold one row for all tokens.   */
+#define MHC_GATE_SIGMOID         0x20u
+#define MHC_WEIGHTS_SHARED       0x40u
 
 /* ---- sizes ------------------------------------------------------------------------------- */
 /* Bytes of the packed projection weights (3 bf16 planes of W_mix plus padding, in the layout
@@ -217,6 +223,95 @@ int mhc_fused_step_backward(const void* X, const void* F, const void* Xp, const 
 /* Workspace bytes of mhc_fused_step_backward on the current device (0 if the shape is
  * unsupported).                                                                               */
 size_t mhc_backward_workspace_bytes(int64_t N, int n, int d);
+
+/* ---- 8-bit activation checkpoints (training) -------------------------------------------------
+ * What a backward pass needs of a sublayer's forward, kept in 8 bits: rows of d features as MXFP8
+ * blocks of 32 consecutive features (the format of mhc_fused_step_mxfp8; d a multiple of 8, the last
+ * block of a row holds the d % 32 features that are left).
+ *   codes uint8 [rows, d]  E4M3;  scales uint8 [rows, ceil(d / 32)]  E8M0
+ * mhc_checkpoint_save: x bf16 [rows, d] -> codes, scales. amax is taken over the finite values of a
+ *   block; an infinity or NaN becomes a NaN code, its neighbours keep their values.
+ * mhc_checkpoint_load: codes, scales -> x bf16 [rows, d] = value(code) 2^(scale - 127), rounded to
+ *   nearest even (exact for every block whose amax was at least 2^-116; scale code 255 gives NaN).
+ * The streams X [N, n, d] are N n rows. 0 <= rows <= 2^40; rows == 0 is MHC_OK. No output may
+ * overlap an input or the other output.                                                       */
+int mhc_checkpoint_save(const void* x, void* codes, void* scales, int64_t rows, int d, void* stream);
+int mhc_checkpoint_load(const void* codes, const void* scales, void* x, int64_t rows, int d,
+                        void* stream);
+/* Bytes of `scales`: rows ceil(d / 32) (0 if the shape is unsupported).                        */
+size_t mhc_checkpoint_scale_bytes(int64_t rows, int d);
+
+/* Gradients of the fused step from checkpoints of its inputs: mhc_fused_step_backward with X and F
+ * replaced by their checkpoints (X_codes uint8 [N, 4, d] and X_scale uint8 [N, 4, d / 32] as
+ * mhc_checkpoint_save writes the N n rows of X, F_codes [N, d] and F_scale [N, d / 32]) and without
+ * X'. The decoded values stand in for X and F, X' = hc_post of them in the forward's float32
+ * arithmetic, rounded to bf16, y_hat = hc_pre(X') rounded to bf16; mixes is the forward's m, whose
+ * gradient g_m is that of the forward. All else as there.
+ * workspace: >= mhc_backward_ckpt_workspace_bytes(N, n, d) device bytes, 16-byte aligned.      */
+int mhc_fused_step_backward_ckpt(const void* X_codes, const void* X_scale, const void* F_codes,
+                                 const void* F_scale, const float* mixes, const float* pre_prev,
+                                 const float* post_prev, const float* comb_prev, const float* W_mix,
+                                 const float* scale, const float* base, const float* gain,
+                                 const void* gXp, const void* gy, const float* gpre,
+                                 const float* gpost, const float* gcomb, void* gX, void* gF,
+                                 float* gpre_prev, float* gpost_prev, float* gcomb_prev, float* gW,
+                                 float* gbase, float* gscale, float* ggain, int64_t N, int n, int d,
+                                 int sinkhorn_iters, float hc_eps, float norm_eps, unsigned flags,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+/* Workspace bytes of mhc_fused_step_backward_ckpt on the current device (0 if the shape is
+ * unsupported).                                                                               */
+size_t mhc_backward_ckpt_workspace_bytes(int64_t N, int n, int d);
+
+/* ---- the norm step: norms before and after a block with its gate and residual scale ----------
+ * The residual step between two blocks with GIVEN stream weights (no mixes), in one pass: the norm
+ * after a block fused with its gate and residual scale, the residual streams, and the norm
+ * before the next block. n = 1 (a plain residual model) or n = 4 streams (weights computed by
+ * mhc_mixes, or static ones with MHC_WEIGHTS_SHARED). Per token:
+ *   Z_i  = res_scale a_i gain_post_i F_i / sqrt(mean(F^2) + norm_eps)
+ *   X'_k = post_k Z + sum_j C_jk X_j   (MHC_COMB_ROW_DEST: sum_j C_kj X_j)      -> X_out
+ *   yh   = sum_k pre_k X'_k,   y = gain_pre yh / sqrt(mean(yh^2) + norm_eps)    -> y_out
+ * in float32 throughout, X' and y each rounded to bf16 once (y is the norm of the unrounded X').
+ *   X bf16 [N, n, d], F bf16 [N, d]
+ *   gate bf16 [N, d] or NULL: a_i = the gate's value, its sigmoid (MHC_GATE_SIGMOID), or 1
+ *   pre, post fp32 [N, n], comb fp32 [N, n, n] ([n], [n], [n, n] with MHC_WEIGHTS_SHARED). With n = 1
+ *     all three may be NULL: X' = X + Z, yh = X'.
+ *   gain_post fp32 [d], or NULL: no norm after the block, Z_i = res_scale a_i F_i
+ *   gain_pre fp32 [d]
+ *   X_out bf16 [N, n, d] (may equal X), y_out bf16 [N, d]
+ * d a multiple of 8, at most 32768. N == 0 returns MHC_OK without launching.                  */
+int mhc_norm_step(const void* X, const void* F, const void* gate, const float* pre, const float* post,
+                  const float* comb, const float* gain_post, const float* gain_pre, void* X_out,
+                  void* y_out, int64_t N, int n, int d, float res_scale, float norm_eps,
+                  unsigned flags, void* stream);
+/* Its gradients from those of X' and y (gXp bf16 [N, n, d], gy bf16 [N, d]), X' recomputed from the
+ * inputs. With G_k = gXp_k + pre_k gyh, gyh the gradient of yh, and q = sum_k post_k G_k:
+ *   gX_j = sum_k C_jk G_k                     bf16 [N, n, d]
+ *   gF   = the gradient of F through Z from q   bf16 [N, d]
+ *   ggate bf16 [N, d]                         with a gate (NULL without)
+ *   gpre_k = gyh . X'_k, gpost_k = G_k . Z, gcomb_jk = G_k . X_j   fp32, shaped like the weights, summed
+ *                                             over the tokens with MHC_WEIGHTS_SHARED (NULL without weights)
+ *   ggain_post, ggain_pre fp32 [d]            sums over the tokens (ggain_post NULL without gain_post)
+ * The sums are written, not accumulated, in a fixed order (the same call gives the same bits); they
+ * are zero when N = 0.
+ * workspace: >= mhc_norm_step_backward_workspace_bytes(N, n, d) device bytes, 16-byte aligned. No
+ * output may overlap an input, the workspace or another output.                               */
+int mhc_norm_step_backward(const void* X, const void* F, const void* gate, const float* pre,
+                           const float* post, const float* comb, const float* gain_post,
+                           const float* gain_pre, const void* gXp, const void* gy, void* gX, void* gF,
+                           void* ggate, float* gpre, float* gpost, float* gcomb, float* ggain_post,
+                           float* ggain_pre, int64_t N, int n, int d, float res_scale, float norm_eps,
+                           unsigned flags, void* workspace, size_t workspace_bytes, void* stream);
+/* The same from checkpoints of X (N n rows) and F (N rows), as mhc_checkpoint_save writes them. */
+int mhc_norm_step_backward_ckpt(const void* X_codes, const void* X_scale, const void* F_codes,
+                                const void* F_scale, const void* gate, const float* pre,
+                                const float* post, const float* comb, const float* gain_post,
+                                const float* gain_pre, const void* gXp, const void* gy, void* gX,
+                                void* gF, void* ggate, float* gpre, float* gpost, float* gcomb,
+                                float* ggain_post, float* ggain_pre, int64_t N, int n, int d,
+                                float res_scale, float norm_eps, unsigned flags, void* workspace,
+                                size_t workspace_bytes, void* stream);
+/* Workspace bytes of both on the current device (0 if the shape is unsupported or N = 0).      */
+size_t mhc_norm_step_backward_workspace_bytes(int64_t N, int n, int d);
 
 /* ---- the fused step without any allocation --------------------------------------------------
  * No counterpart in the paper: an addition for callers that cannot allocate device memory when

@@ -1,0 +1,105 @@
+"""The norm step and its gradients in float64 (oracle; test infrastructure only).
+
+Per token, with F a block's output, a its gate, s the residual scale and n streams X:
+    Z = s a gain_post F r_F,        r_F = (mean F^2 + eps)^(-1/2)   (no post norm: Z = s a F)
+    X'_k = u_k Z + sum_j C_jk X_j   (the other reading of comb: C transposed)
+    yh = sum_k p_k X'_k,  y = gain_pre yh r_y,  r_y = (mean yh^2 + eps)^(-1/2)
+`weights` None is one stream with weights of 1.
+
+Beside each result the functions return its magnitude: the same formula with every term replaced by
+its absolute value. A float32 evaluation whose longest chain of roundings is c long is within
+about c 2^-24 of that magnitude, whatever cancels.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+__all__ = ["norm_step", "norm_step_backward"]
+
+
+def _f64(a):
+    return np.asarray(a, dtype=np.float64)
+
+
+def _parts(X, F, gain_post, gate, weights, scale, eps, sigmoid, row_dest):
+    X, F = _f64(X), _f64(F)
+    N, n, d = X.shape
+    if weights is None:
+        p, u, C = np.ones((N, n)), np.ones((N, n)), np.ones((N, n, n))
+    else:
+        p, u, C = (np.broadcast_to(_f64(w), s) for w, s in zip(weights, ((N, n), (N, n), (N, n, n))))
+    C = np.swapaxes(C, 1, 2) if row_dest else C
+    if gate is None:
+        a, da = np.ones((N, d)), np.zeros((N, d))
+    elif sigmoid:
+        a = 1.0 / (1.0 + np.exp(-_f64(gate)))
+        da = a * (1.0 - a)
+    else:
+        a, da = _f64(gate), np.ones((N, d))
+    if gain_post is None:
+        r, k = np.ones((N, 1)), np.ones(d)
+    else:
+        r = 1.0 / np.sqrt((F * F).mean(axis=1, keepdims=True) + eps)
+        k = _f64(gain_post)
+    Z = scale * a * k * F * r
+    Xp = np.einsum("njk,njd->nkd", C, X) + u[:, :, None] * Z[:, None, :]
+    mag = np.einsum("njk,njd->nkd", np.abs(C), np.abs(X)) + np.abs(u)[:, :, None] * np.abs(Z)[:, None, :]
+    yh = np.einsum("nk,nkd->nd", p, Xp)
+    yh_mag = np.einsum("nk,nkd->nd", np.abs(p), mag)
+    ry = 1.0 / np.sqrt((yh * yh).mean(axis=1, keepdims=True) + eps)
+    # the relative error of r_y is that of mean yh^2, whose terms are off by yh_mag each
+    ry_mag = ry * (1.0 + ry * ry * (np.abs(yh) * yh_mag).mean(axis=1, keepdims=True))
+    return X, F, p, u, C, a, da, r, k, Z, Xp, mag, yh, yh_mag, ry, ry_mag
+
+
+def norm_step(X, F, gain_post, gain_pre, *, gate=None, weights=None, scale=1.0, eps=1e-6, sigmoid=False,
+              row_dest=False):
+    """({Xp, y}, their magnitudes)."""
+    *_, Xp, mag, yh, yh_mag, ry, ry_mag = _parts(X, F, gain_post, gate, weights, scale, eps, sigmoid, row_dest)
+    g = _f64(gain_pre)
+    return ({"Xp": Xp, "y": g * yh * ry},
+            {"Xp": mag, "y": np.abs(g) * (yh_mag * ry + np.abs(yh) * ry_mag)})
+
+
+def norm_step_backward(X, F, gXp, gy, gain_post, gain_pre, *, gate=None, weights=None, scale=1.0, eps=1e-6,
+                       sigmoid=False, row_dest=False, shared=False):
+    """({gX, gF, ggain_pre, ...}, their magnitudes); the sums over tokens of gpre, gpost and gcomb where
+    `shared`."""
+    X, F, p, u, C, a, da, r, k, Z, Xp, mag, yh, yh_mag, ry, ry_mag = _parts(
+        X, F, gain_post, gate, weights, scale, eps, sigmoid, row_dest)
+    gXp, gy, g = _f64(gXp), _f64(gy), _f64(gain_pre)
+    A = np.abs
+    T = (g * gy * yh).mean(axis=1, keepdims=True)
+    T_mag = (A(g * gy) * (yh_mag + A(yh))).mean(axis=1, keepdims=True)
+    gyh = ry * g * gy - ry ** 3 * T * yh
+    gyh_mag = ry_mag * A(g * gy) + ry ** 2 * (ry * (T_mag * A(yh) + A(T) * yh_mag) + 3 * ry_mag * A(T * yh))
+    G = gXp + p[:, :, None] * gyh[:, None, :]
+    Gm = A(gXp) + A(p)[:, :, None] * gyh_mag[:, None, :]
+    q, qm = np.einsum("nk,nkd->nd", u, G), np.einsum("nk,nkd->nd", A(u), Gm)
+    h = scale * a * k
+    out = {"gX": np.einsum("njk,nkd->njd", C, G)}
+    m = {"gX": np.einsum("njk,nkd->njd", A(C), Gm)}
+    if gain_post is None:
+        out["gF"], m["gF"] = h * q, A(h) * qm
+    else:
+        S, Sm = (h * q * F).mean(axis=1, keepdims=True), (A(h * F) * qm).mean(axis=1, keepdims=True)
+        out["gF"] = r * h * q - r ** 3 * S * F
+        m["gF"] = r * A(h) * qm + r ** 3 * Sm * A(F)
+        out["ggain_post"], m["ggain_post"] = (scale * a * F * r * q).sum(0), (A(scale * a * F * r) * qm).sum(0)
+    if gate is not None:
+        out["ggate"], m["ggate"] = scale * k * F * r * q * da, A(scale * k * F * r * da) * qm
+        if sigmoid:   # 1 - a is off by a rounding of a, however small it is
+            m["ggate"] = m["ggate"] + A(scale * k * F * r * q * a)
+    out["ggain_pre"] = (gy * yh * ry).sum(0)
+    m["ggain_pre"] = (A(gy) * (yh_mag * ry + A(yh) * ry_mag)).sum(0)
+    if weights is not None:
+        gC, gCm = np.einsum("nkd,njd->njk", G, X), np.einsum("nkd,njd->njk", Gm, A(X))
+        if row_dest:
+            gC, gCm = np.swapaxes(gC, 1, 2), np.swapaxes(gCm, 1, 2)
+        per = {"gpre": (np.einsum("nd,nkd->nk", gyh, Xp),
+                        np.einsum("nd,nkd->nk", gyh_mag, A(Xp)) + np.einsum("nd,nkd->nk", A(gyh), mag)),
+               "gpost": (np.einsum("nkd,nd->nk", G, Z), np.einsum("nkd,nd->nk", Gm, A(Z))),
+               "gcomb": (gC, gCm)}
+        for key, (v, vm) in per.items():
+            out[key], m[key] = (v.sum(0), vm.sum(0)) if shared else (v, vm)
+    return out, m

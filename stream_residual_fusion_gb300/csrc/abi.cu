@@ -154,6 +154,172 @@ int fused_common(const void* X, const void* F, const float* pre_prev, const floa
   return cuda_code(launch_step(true, a, s));
 }
 
+// Checks and launch shared by the two backward entries: from X, F and X', or (`c` set) from
+// checkpoints of X and F.
+int backward_common(const BwdArgs& a, int n, const BwdCheckpoint* c, void* stream) {
+  const int64_t N = a.N;
+  const int d = a.d;
+  if (n != 4 || N < 0 || N > kMaxTokens || d <= 0 || d % 64 != 0 || a.iters < 1) return MHC_ERR_SHAPE;
+  if ((a.flags & ~MHC_COMB_ROW_DEST) != 0) return MHC_ERR_SHAPE;
+  if (!a.W || !a.scale || !a.base || !a.gain || !a.gW || !a.gbase || !a.gscale || !a.ggain) return MHC_ERR_NULL;
+  const void* params[] = {a.W, a.scale, a.base, a.gain, a.gW, a.gbase, a.gscale, a.ggain};
+  for (const void* p : params)
+    if (!aligned16(p)) return MHC_ERR_ALIGN;
+  const uint64_t nt = static_cast<uint64_t>(N), K = 4ull * d;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {   // sums over no tokens
+    const Span pin[] = {span(a.W, 96 * K), span(a.scale, 12), span(a.base, 96), span(a.gain, 4ull * d)};
+    const Span pout[] = {span(a.gW, 96 * K), span(a.gbase, 96), span(a.gscale, 12), span(a.ggain, 4ull * d)};
+    if (!aliasing_ok(pout, pin)) return MHC_ERR_ALIAS;
+    cudaError_t e = cudaMemsetAsync(a.gW, 0, 96 * K, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(a.gbase, 0, 96, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(a.gscale, 0, 12, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(a.ggain, 0, 4ull * d, s);
+    return cuda_code(e);
+  }
+  const void* saved[] = {c ? c->X_codes : a.X, c ? c->F_codes : a.F, c ? c->X_scale : a.Xp, c ? c->F_scale : a.F};
+  const uint64_t saved_bytes[] = {nt * K * (c ? 1 : 2), nt * d * (c ? 1 : 2), c ? nt * K / 32 : nt * K * 2,
+                                  c ? nt * d / 32 : nt * d * 2};
+  const void* ptrs[] = {saved[0], saved[1], saved[2], saved[3], a.mixes, a.pre_prev, a.post_prev, a.comb_prev,
+                        a.gXp, a.gy, a.gpre, a.gpost, a.gcomb, a.gX, a.gF, a.gpre_prev, a.gpost_prev,
+                        a.gcomb_prev};
+  for (const void* p : ptrs)
+    if (!p) return MHC_ERR_NULL;
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return MHC_ERR_ALIGN;
+  if (!a.workspace) return MHC_ERR_WORKSPACE;
+  if (!aligned16(a.workspace)) return MHC_ERR_ALIGN;
+  const Span ins[] = {span(saved[0], saved_bytes[0]), span(saved[1], saved_bytes[1]),
+                      span(saved[2], saved_bytes[2]), span(saved[3], saved_bytes[3]),
+                      span(a.mixes, nt * 96),     span(a.pre_prev, nt * 16),   span(a.post_prev, nt * 16),
+                      span(a.comb_prev, nt * 64), span(a.W, 96 * K),           span(a.scale, 12),
+                      span(a.base, 96),           span(a.gain, 4ull * d),      span(a.gXp, nt * K * 2),
+                      span(a.gy, nt * d * 2),     span(a.gpre, nt * 16),       span(a.gpost, nt * 16),
+                      span(a.gcomb, nt * 64)};
+  const Span outs[] = {span(a.gX, nt * K * 2),      span(a.gF, nt * d * 2),      span(a.gpre_prev, nt * 16),
+                       span(a.gpost_prev, nt * 16), span(a.gcomb_prev, nt * 64), span(a.gW, 96 * K),
+                       span(a.gbase, 96),           span(a.gscale, 12),          span(a.ggain, 4ull * d),
+                       span(a.workspace, a.workspace_bytes)};
+  if (!aliasing_ok(outs, ins)) return MHC_ERR_ALIAS;
+  const size_t need = c ? bwd_ckpt_bytes(N, d) : bwd_layout(N, d).bytes;
+  if (need == 0) return MHC_ERR_CUDA;
+  if (a.workspace_bytes < need) return MHC_ERR_WORKSPACE;
+  return cuda_code(c ? launch_backward_ckpt(a, *c, s) : launch_backward(a, s));
+}
+
+constexpr int64_t kMaxRows = int64_t(1) << 40;   // rows of a checkpoint
+
+// Shape, flags, weights and parameters of a norm step (either direction).
+int check_norm(const NormArgs& a) {
+  if ((a.n != 1 && a.n != 4) || a.N < 0 || a.N > kMaxTokens || a.d <= 0 || a.d % 8 != 0 || a.d > kNormMaxWidth)
+    return MHC_ERR_SHAPE;
+  if ((a.flags & ~(MHC_COMB_ROW_DEST | MHC_GATE_SIGMOID | MHC_WEIGHTS_SHARED)) != 0) return MHC_ERR_SHAPE;
+  if (!a.gain_pre) return MHC_ERR_NULL;
+  const void* params[] = {a.gain_pre, a.gain_post, a.gate, a.pre, a.post, a.comb};
+  for (const void* p : params)
+    if (p && !aligned16(p)) return MHC_ERR_ALIGN;
+  if (a.N == 0) return MHC_OK;
+  if ((a.flags & MHC_GATE_SIGMOID) && !a.gate) return MHC_ERR_NULL;
+  // weights: all three, or none of them for one stream
+  const bool any = a.pre || a.post || a.comb, all = a.pre && a.post && a.comb;
+  if (any ? !all : (a.n != 1 || (a.flags & MHC_WEIGHTS_SHARED))) return MHC_ERR_NULL;
+  return MHC_OK;
+}
+
+struct NormBytes {
+  uint64_t streams, rows, pre, comb, gain;
+};
+NormBytes norm_bytes(const NormArgs& a) {
+  const uint64_t nt = static_cast<uint64_t>(a.N), n = static_cast<uint64_t>(a.n), d = static_cast<uint64_t>(a.d);
+  const uint64_t wt = a.pre == nullptr ? 0 : (a.flags & MHC_WEIGHTS_SHARED) ? 1 : nt;
+  return NormBytes{2 * nt * n * d, 2 * nt * d, 4 * wt * n, 4 * wt * n * n, 4 * d};
+}
+
+int norm_backward_common(const void* X, const void* X_scale, const void* F, const void* F_scale, bool ckpt,
+                         const void* gate, const float* pre, const float* post, const float* comb,
+                         const float* gain_post, const float* gain_pre, const void* gXp, const void* gy,
+                         void* gX, void* gF, void* ggate, float* gpre, float* gpost, float* gcomb,
+                         float* ggain_post, float* ggain_pre, int64_t N, int n, int d, float res_scale,
+                         float norm_eps, unsigned flags, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  NormArgs a{};
+  a.X = X;
+  a.F = F;
+  a.X_scale = static_cast<const uint8_t*>(X_scale);
+  a.F_scale = static_cast<const uint8_t*>(F_scale);
+  a.gate = gate;
+  a.pre = pre;
+  a.post = post;
+  a.comb = comb;
+  a.gain_post = gain_post;
+  a.gain_pre = gain_pre;
+  a.gXp = gXp;
+  a.gy = gy;
+  a.gX = gX;
+  a.gF = gF;
+  a.ggate = ggate;
+  a.gpre = gpre;
+  a.gpost = gpost;
+  a.gcomb = gcomb;
+  a.ggain_post = ggain_post;
+  a.ggain_pre = ggain_pre;
+  a.partial = static_cast<float*>(workspace);
+  a.N = N;
+  a.n = n;
+  a.d = d;
+  a.res_scale = res_scale;
+  a.eps = norm_eps;
+  a.flags = flags;
+  const int rc = check_norm(a);
+  if (rc != MHC_OK) return rc;
+  const bool shared = (flags & MHC_WEIGHTS_SHARED) != 0, weights = pre != nullptr;
+  // gradients that are summed over the tokens exist for N = 0 too
+  if (!ggain_pre || (gain_post && !ggain_post) || (weights && shared && (!gpre || !gpost || !gcomb)))
+    return MHC_ERR_NULL;
+  const void* sums[] = {ggain_pre, gain_post ? ggain_post : nullptr, weights ? gpre : nullptr,
+                        weights ? gpost : nullptr, weights ? gcomb : nullptr};
+  for (const void* p : sums)
+    if (p && !aligned16(p)) return MHC_ERR_ALIGN;
+  const NormBytes b = norm_bytes(a);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    const uint64_t wp = weights && shared ? 4ull * n : 0, wc = weights && shared ? 4ull * n * n : 0;
+    const Span pin[] = {span(gain_post, gain_post ? b.gain : 0), span(gain_pre, b.gain), span(pre, wp),
+                        span(post, wp), span(comb, wc)};
+    const Span pout[] = {span(ggain_pre, b.gain), span(ggain_post, gain_post ? b.gain : 0), span(gpre, wp),
+                         span(gpost, wp), span(gcomb, wc)};
+    if (!aliasing_ok(pout, pin)) return MHC_ERR_ALIAS;
+    cudaError_t e = cudaMemsetAsync(ggain_pre, 0, b.gain, s);
+    if (e == cudaSuccess && gain_post) e = cudaMemsetAsync(ggain_post, 0, b.gain, s);
+    if (e == cudaSuccess && wp) e = cudaMemsetAsync(gpre, 0, wp, s);
+    if (e == cudaSuccess && wp) e = cudaMemsetAsync(gpost, 0, wp, s);
+    if (e == cudaSuccess && wc) e = cudaMemsetAsync(gcomb, 0, wc, s);
+    return cuda_code(e);
+  }
+  if (!X || !F || (ckpt && (!X_scale || !F_scale)) || !gXp || !gy || !gX || !gF || (gate && !ggate) ||
+      (weights && (!gpre || !gpost || !gcomb)))
+    return MHC_ERR_NULL;
+  const void* ptrs[] = {X, F, X_scale, F_scale, gXp, gy, gX, gF, gate ? ggate : nullptr};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return MHC_ERR_ALIGN;
+  if (!workspace) return MHC_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MHC_ERR_ALIGN;
+  const uint64_t rows = static_cast<uint64_t>(N), blocks = (static_cast<uint64_t>(d) + 31) / 32;
+  const Span ins[] = {span(X, ckpt ? b.streams / 2 : b.streams), span(F, ckpt ? b.rows / 2 : b.rows),
+                      span(X_scale, ckpt ? rows * n * blocks : 0), span(F_scale, ckpt ? rows * blocks : 0),
+                      span(gate, gate ? b.rows : 0), span(pre, b.pre), span(post, b.pre), span(comb, b.comb),
+                      span(gain_post, gain_post ? b.gain : 0), span(gain_pre, b.gain),
+                      span(gXp, b.streams), span(gy, b.rows)};
+  const Span outs[] = {span(gX, b.streams), span(gF, b.rows), span(ggate, gate ? b.rows : 0), span(gpre, b.pre),
+                       span(gpost, b.pre), span(gcomb, b.comb), span(ggain_post, gain_post ? b.gain : 0),
+                       span(ggain_pre, b.gain), span(workspace, workspace_bytes)};
+  if (!aliasing_ok(outs, ins)) return MHC_ERR_ALIAS;
+  const size_t need = mhc_norm_step_backward_workspace_bytes(N, n, d);
+  if (need == 0) return MHC_ERR_CUDA;
+  if (workspace_bytes < need) return MHC_ERR_WORKSPACE;
+  return cuda_code(launch_norm_step_backward(a, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -477,47 +643,6 @@ int mhc_fused_step_backward(const void* X, const void* F, const void* Xp, const 
                             float* gbase, float* gscale, float* ggain, int64_t N, int n, int d,
                             int sinkhorn_iters, float hc_eps, float norm_eps, unsigned flags,
                             void* workspace, size_t workspace_bytes, void* stream) {
-  if (n != 4 || N < 0 || N > kMaxTokens || d <= 0 || d % 64 != 0 || sinkhorn_iters < 1)
-    return MHC_ERR_SHAPE;
-  if ((flags & ~MHC_COMB_ROW_DEST) != 0) return MHC_ERR_SHAPE;
-  if (!W_mix || !scale || !base || !gain || !gW || !gbase || !gscale || !ggain) return MHC_ERR_NULL;
-  const void* params[] = {W_mix, scale, base, gain, gW, gbase, gscale, ggain};
-  for (const void* p : params)
-    if (!aligned16(p)) return MHC_ERR_ALIGN;
-  const uint64_t nt = static_cast<uint64_t>(N), K = 4ull * d;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (N == 0) {   // sums over no tokens
-    const Span pin[] = {span(W_mix, 96 * K), span(scale, 12), span(base, 96), span(gain, 4ull * d)};
-    const Span pout[] = {span(gW, 96 * K), span(gbase, 96), span(gscale, 12), span(ggain, 4ull * d)};
-    if (!aliasing_ok(pout, pin)) return MHC_ERR_ALIAS;
-    cudaError_t e = cudaMemsetAsync(gW, 0, 96 * K, s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(gbase, 0, 96, s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(gscale, 0, 12, s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(ggain, 0, 4ull * d, s);
-    return cuda_code(e);
-  }
-  const void* ptrs[] = {X, F, Xp, mixes, pre_prev, post_prev, comb_prev, gXp, gy, gpre, gpost,
-                        gcomb, gX, gF, gpre_prev, gpost_prev, gcomb_prev};
-  for (const void* p : ptrs)
-    if (!p) return MHC_ERR_NULL;
-  for (const void* p : ptrs)
-    if (!aligned16(p)) return MHC_ERR_ALIGN;
-  if (!workspace) return MHC_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return MHC_ERR_ALIGN;
-  const Span ins[] = {span(X, nt * K * 2),      span(F, nt * d * 2),       span(Xp, nt * K * 2),
-                      span(mixes, nt * 96),     span(pre_prev, nt * 16),   span(post_prev, nt * 16),
-                      span(comb_prev, nt * 64), span(W_mix, 96 * K),       span(scale, 12),
-                      span(base, 96),           span(gain, 4ull * d),      span(gXp, nt * K * 2),
-                      span(gy, nt * d * 2),     span(gpre, nt * 16),       span(gpost, nt * 16),
-                      span(gcomb, nt * 64)};
-  const Span outs[] = {span(gX, nt * K * 2),      span(gF, nt * d * 2),     span(gpre_prev, nt * 16),
-                       span(gpost_prev, nt * 16), span(gcomb_prev, nt * 64), span(gW, 96 * K),
-                       span(gbase, 96),           span(gscale, 12),         span(ggain, 4ull * d),
-                       span(workspace, workspace_bytes)};
-  if (!aliasing_ok(outs, ins)) return MHC_ERR_ALIAS;
-  const size_t need = bwd_layout(N, d).bytes;
-  if (need == 0) return MHC_ERR_CUDA;
-  if (workspace_bytes < need) return MHC_ERR_WORKSPACE;
   BwdArgs a{};
   a.X = X;
   a.F = F;
@@ -552,7 +677,161 @@ int mhc_fused_step_backward(const void* X, const void* F, const void* Xp, const 
   a.hc_eps = hc_eps;
   a.norm_eps = norm_eps;
   a.flags = flags;
-  return cuda_code(launch_backward(a, s));
+  return backward_common(a, n, nullptr, stream);
+}
+
+size_t mhc_backward_ckpt_workspace_bytes(int64_t N, int n, int d) {
+  if (n != 4 || N < 0 || N > kMaxTokens || d <= 0 || d % 64 != 0) return 0;
+  return bwd_ckpt_bytes(N, d);
+}
+
+int mhc_fused_step_backward_ckpt(const void* X_codes, const void* X_scale, const void* F_codes,
+                                 const void* F_scale, const float* mixes, const float* pre_prev,
+                                 const float* post_prev, const float* comb_prev, const float* W_mix,
+                                 const float* scale, const float* base, const float* gain,
+                                 const void* gXp, const void* gy, const float* gpre,
+                                 const float* gpost, const float* gcomb, void* gX, void* gF,
+                                 float* gpre_prev, float* gpost_prev, float* gcomb_prev, float* gW,
+                                 float* gbase, float* gscale, float* ggain, int64_t N, int n, int d,
+                                 int sinkhorn_iters, float hc_eps, float norm_eps, unsigned flags,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  BwdCheckpoint c{};
+  c.X_codes = X_codes;
+  c.X_scale = X_scale;
+  c.F_codes = F_codes;
+  c.F_scale = F_scale;
+  BwdArgs a{};
+  a.mixes = mixes;
+  a.pre_prev = pre_prev;
+  a.post_prev = post_prev;
+  a.comb_prev = comb_prev;
+  a.W = W_mix;
+  a.scale = scale;
+  a.base = base;
+  a.gain = gain;
+  a.gXp = gXp;
+  a.gy = gy;
+  a.gpre = gpre;
+  a.gpost = gpost;
+  a.gcomb = gcomb;
+  a.gX = gX;
+  a.gF = gF;
+  a.gpre_prev = gpre_prev;
+  a.gpost_prev = gpost_prev;
+  a.gcomb_prev = gcomb_prev;
+  a.gW = gW;
+  a.gbase = gbase;
+  a.gscale = gscale;
+  a.ggain = ggain;
+  a.workspace = workspace;
+  a.workspace_bytes = workspace_bytes;
+  a.N = N;
+  a.d = d;
+  a.iters = sinkhorn_iters;
+  a.hc_eps = hc_eps;
+  a.norm_eps = norm_eps;
+  a.flags = flags;
+  return backward_common(a, n, &c, stream);
+}
+
+// ---------------------------------------------------------------------------------------------
+// Activation checkpoints.
+
+size_t mhc_checkpoint_scale_bytes(int64_t rows, int d) {
+  if (rows < 0 || rows > kMaxRows || d <= 0 || d % 8 != 0) return 0;
+  return static_cast<size_t>(rows) * ((static_cast<size_t>(d) + 31) / 32);
+}
+
+int mhc_checkpoint_save(const void* x, void* codes, void* scales, int64_t rows, int d, void* stream) {
+  if (rows < 0 || rows > kMaxRows || d <= 0 || d % 8 != 0) return MHC_ERR_SHAPE;
+  if (rows == 0) return MHC_OK;
+  if (!x || !codes || !scales) return MHC_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MHC_ERR_ALIGN;
+  const uint64_t e = static_cast<uint64_t>(rows) * d;
+  const Span ins[] = {span(x, 2 * e)};
+  const Span outs[] = {span(codes, e), span(scales, mhc_checkpoint_scale_bytes(rows, d))};
+  if (!aliasing_ok(outs, ins)) return MHC_ERR_ALIAS;
+  return cuda_code(launch_checkpoint_save(x, codes, scales, rows, d, static_cast<cudaStream_t>(stream)));
+}
+
+int mhc_checkpoint_load(const void* codes, const void* scales, void* x, int64_t rows, int d, void* stream) {
+  if (rows < 0 || rows > kMaxRows || d <= 0 || d % 8 != 0) return MHC_ERR_SHAPE;
+  if (rows == 0) return MHC_OK;
+  if (!x || !codes || !scales) return MHC_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MHC_ERR_ALIGN;
+  const uint64_t e = static_cast<uint64_t>(rows) * d;
+  const Span ins[] = {span(codes, e), span(scales, mhc_checkpoint_scale_bytes(rows, d))};
+  const Span outs[] = {span(x, 2 * e)};
+  if (!aliasing_ok(outs, ins)) return MHC_ERR_ALIAS;
+  return cuda_code(launch_checkpoint_load(codes, scales, x, rows, d, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------------------------
+// The norm step.
+
+int mhc_norm_step(const void* X, const void* F, const void* gate, const float* pre, const float* post,
+                  const float* comb, const float* gain_post, const float* gain_pre, void* X_out,
+                  void* y_out, int64_t N, int n, int d, float res_scale, float norm_eps,
+                  unsigned flags, void* stream) {
+  NormArgs a{};
+  a.X = X;
+  a.F = F;
+  a.gate = gate;
+  a.pre = pre;
+  a.post = post;
+  a.comb = comb;
+  a.gain_post = gain_post;
+  a.gain_pre = gain_pre;
+  a.X_out = X_out;
+  a.y = y_out;
+  a.N = N;
+  a.n = n;
+  a.d = d;
+  a.res_scale = res_scale;
+  a.eps = norm_eps;
+  a.flags = flags;
+  int rc = check_norm(a);
+  if (rc != MHC_OK || N == 0) return rc;
+  if (!X || !F || !X_out || !y_out) return MHC_ERR_NULL;
+  const void* ptrs[] = {X, F, X_out, y_out};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return MHC_ERR_ALIGN;
+  const NormBytes b = norm_bytes(a);
+  const Span ins[] = {span(X, b.streams),   span(F, b.rows),       span(gate, gate ? b.rows : 0),
+                      span(pre, b.pre),     span(post, b.pre),     span(comb, b.comb),
+                      span(gain_post, gain_post ? b.gain : 0),     span(gain_pre, b.gain)};
+  const Span outs[] = {span(X_out, b.streams), span(y_out, b.rows)};
+  if (!aliasing_ok(outs, ins, 0, 0)) return MHC_ERR_ALIAS;
+  return cuda_code(launch_norm_step(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mhc_norm_step_backward_workspace_bytes(int64_t N, int n, int d) {
+  if ((n != 1 && n != 4) || N < 0 || N > kMaxTokens || d <= 0 || d % 8 != 0 || d > kNormMaxWidth) return 0;
+  return static_cast<size_t>(norm_backward_rows(N)) * norm_partial_floats(d) * 4;
+}
+
+int mhc_norm_step_backward(const void* X, const void* F, const void* gate, const float* pre,
+                           const float* post, const float* comb, const float* gain_post,
+                           const float* gain_pre, const void* gXp, const void* gy, void* gX, void* gF,
+                           void* ggate, float* gpre, float* gpost, float* gcomb, float* ggain_post,
+                           float* ggain_pre, int64_t N, int n, int d, float res_scale, float norm_eps,
+                           unsigned flags, void* workspace, size_t workspace_bytes, void* stream) {
+  return norm_backward_common(X, nullptr, F, nullptr, false, gate, pre, post, comb, gain_post, gain_pre,
+                              gXp, gy, gX, gF, ggate, gpre, gpost, gcomb, ggain_post, ggain_pre, N, n, d,
+                              res_scale, norm_eps, flags, workspace, workspace_bytes, stream);
+}
+
+int mhc_norm_step_backward_ckpt(const void* X_codes, const void* X_scale, const void* F_codes,
+                                const void* F_scale, const void* gate, const float* pre,
+                                const float* post, const float* comb, const float* gain_post,
+                                const float* gain_pre, const void* gXp, const void* gy, void* gX,
+                                void* gF, void* ggate, float* gpre, float* gpost, float* gcomb,
+                                float* ggain_post, float* ggain_pre, int64_t N, int n, int d,
+                                float res_scale, float norm_eps, unsigned flags, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  return norm_backward_common(X_codes, X_scale, F_codes, F_scale, true, gate, pre, post, comb, gain_post,
+                              gain_pre, gXp, gy, gX, gF, ggate, gpre, gpost, gcomb, ggain_post, ggain_pre,
+                              N, n, d, res_scale, norm_eps, flags, workspace, workspace_bytes, stream);
 }
 
 int mhc_set_trace(void* buffer, int64_t bytes) {

@@ -41,6 +41,7 @@
 #include "hc_arith.cuh"
 #include "internal.h"
 #include "layout.cuh"
+#include "mx8.cuh"
 #include "ptx.cuh"
 
 namespace mhc {
@@ -1056,6 +1057,58 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(
 }
 
 // ---------------------------------------------------------------------------------------------
+// Checkpoints of X and F to bf16 X, F and X' = hc_post(X, F): one thread per 8 columns of a token.
+__global__ void expand_kernel(const uint2* __restrict__ Xc, const uint8_t* __restrict__ Xs,
+                              const uint2* __restrict__ Fc, const uint8_t* __restrict__ Fs,
+                              const float* __restrict__ post, const float* __restrict__ comb,
+                              uint4* __restrict__ X, uint4* __restrict__ F, uint4* __restrict__ Xp,
+                              int64_t N, int d, int row_dest, float neg_zero) {
+  const int chunks = d / 8, blocks = d / MX_BLOCK;
+  const int64_t total = N * chunks;
+  for (int64_t idx = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; idx < total;
+       idx += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t t = idx / chunks;
+    const int c = static_cast<int>(idx - t * chunks);
+    auto rows = [&](const uint2* codes, const uint8_t* scales, int64_t row, f2 (&v)[4]) {
+      const uint2 w = __ldg(codes + row * chunks + c);
+      const float sv = scale_value(__ldg(scales + row * blocks + c / 4));
+      const f2 s{sv, sv};
+      v[0] = decode2(w.x, s);
+      v[1] = decode2(w.x >> 16, s);
+      v[2] = decode2(w.y, s);
+      v[3] = decode2(w.y >> 16, s);
+    };
+    f2 x[4][4], f[4];
+    rows(Fc, Fs, t, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rows(Xc, Xs, t * 4 + j, x[j]);
+    uint32_t o[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float uk = __ldg(post + t * 4 + k);
+      f2 ck[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v = __ldg(comb + t * 16 + (row_dest ? k * 4 + j : j * 4 + k));
+        ck[j] = f2{v, v};
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const f2 xw[4] = {x[0][w], x[1][w], x[2][w], x[3][w]};
+        o[k][w] = f2_to_bf2(hc_post_pair(ck, f2{uk, uk}, xw, f[w], f2{neg_zero, neg_zero}));
+      }
+    }
+    F[idx] = make_uint4(f2_to_bf2(f[0]), f2_to_bf2(f[1]), f2_to_bf2(f[2]), f2_to_bf2(f[3]));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = (t * 4 + k) * chunks + c;
+      X[at] = make_uint4(f2_to_bf2(x[k][0]), f2_to_bf2(x[k][1]), f2_to_bf2(x[k][2]), f2_to_bf2(x[k][3]));
+      Xp[at] = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
 // host side
 
 // No L2 promotion: a CTA of these kernels reads the neighbouring columns of a row only slots
@@ -1237,6 +1290,34 @@ cudaError_t launch_backward(const BwdArgs& a, cudaStream_t stream) {
                                                   a.ggain, a.gbase, a.gscale, d, L.ranges, L.blocks0);
   }
   return cudaGetLastError();
+}
+
+size_t bwd_ckpt_bytes(int64_t N, int d) {
+  const size_t base = bwd_layout(N, d).bytes;
+  if (base == 0) return 0;
+  const size_t streams = a256(static_cast<size_t>(N) * 8 * d), rows = a256(static_cast<size_t>(N) * 2 * d);
+  return a256(base) + 2 * streams + rows;
+}
+
+cudaError_t launch_backward_ckpt(const BwdArgs& args, const BwdCheckpoint& c, cudaStream_t stream) {
+  BwdArgs a = args;
+  const size_t base = a256(bwd_layout(a.N, a.d).bytes);
+  const size_t streams = a256(static_cast<size_t>(a.N) * 8 * a.d);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  uint4* X = reinterpret_cast<uint4*>(ws + base);
+  uint4* Xp = reinterpret_cast<uint4*>(ws + base + streams);
+  uint4* F = reinterpret_cast<uint4*>(ws + base + 2 * streams);
+  const int64_t work = a.N * (a.d / 8);
+  expand_kernel<<<static_cast<int>(std::min<int64_t>((work + 255) / 256, 16 * sm_count())), 256, 0, stream>>>(
+      static_cast<const uint2*>(c.X_codes), static_cast<const uint8_t*>(c.X_scale),
+      static_cast<const uint2*>(c.F_codes), static_cast<const uint8_t*>(c.F_scale), a.post_prev, a.comb_prev, X,
+      F, Xp, a.N, a.d, static_cast<int>(a.flags & 1u), -0.0f);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  a.X = X;
+  a.F = F;
+  a.Xp = Xp;
+  return launch_backward(a, stream);
 }
 
 }  // namespace mhc

@@ -168,6 +168,65 @@ struct BwdLayout {
 BwdLayout bwd_layout(int64_t N, int d);
 cudaError_t launch_backward(const BwdArgs& a, cudaStream_t stream);
 
+// Gradients of the step from MXFP8 checkpoints of X and F (BwdArgs.X, F and Xp unused).
+struct BwdCheckpoint {
+  const void* X_codes;    // uint8 [N, 4, d]
+  const void* X_scale;    // uint8 [N, 4, d / 32]
+  const void* F_codes;    // uint8 [N, d]
+  const void* F_scale;    // uint8 [N, d / 32]
+};
+// Its workspace; 0 like bwd_layout.
+size_t bwd_ckpt_bytes(int64_t N, int d);
+cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& c, cudaStream_t stream);
+
+// Activation checkpoints (checkpoint.cu): bf16 rows of d features to MXFP8 and back.
+cudaError_t launch_checkpoint_save(const void* x, void* codes, void* scales, int64_t rows, int d,
+                                   cudaStream_t stream);
+cudaError_t launch_checkpoint_load(const void* codes, const void* scales, void* x, int64_t rows, int d,
+                                   cudaStream_t stream);
+
+// The norm step and its gradients (norm_step.cu).
+constexpr unsigned FLAG_GATE_SIGMOID = 0x20u;
+constexpr unsigned FLAG_WEIGHTS_SHARED = 0x40u;
+constexpr int kNormMaxWidth = 32768;
+struct NormArgs {
+  const void* X;            // bf16 [N, n, d], or E4M3 codes with X_scale
+  const void* F;            // bf16 [N, d], or E4M3 codes with F_scale
+  const uint8_t* X_scale;   // backward from checkpoints only
+  const uint8_t* F_scale;
+  const void* gate;         // bf16 [N, d] or null
+  const float* pre;         // [N, n] ([n] with FLAG_WEIGHTS_SHARED); null with n = 1: weights of 1
+  const float* post;
+  const float* comb;
+  const float* gain_post;   // [d] or null: no norm after the block
+  const float* gain_pre;    // [d]
+  void* X_out;              // forward
+  void* y;
+  const void* gXp;          // backward
+  const void* gy;
+  void* gX;
+  void* gF;
+  void* ggate;
+  float* gpre;
+  float* gpost;
+  float* gcomb;
+  float* ggain_post;
+  float* ggain_pre;
+  float* partial;           // norm_backward_rows(N) rows of norm_partial_floats(d)
+  int64_t N;
+  int n;
+  int d;
+  float res_scale;
+  float eps;
+  unsigned flags;
+};
+// Floats of one row of the backward's partial sums: ggain_pre [d], ggain_post [d], shared weights.
+__host__ __device__ constexpr int norm_partial_floats(int d) { return 2 * d + 32; }
+// Rows of partial sums the backward writes for N tokens on the current device (0: no device).
+int norm_backward_rows(int64_t N);
+cudaError_t launch_norm_step(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_step_backward(const NormArgs& a, cudaStream_t stream);
+
 // Address ranges of the tensors of a call, for the overlap checks of the entry points.
 struct Span {
   uintptr_t lo, hi;

@@ -10,7 +10,9 @@ lists; outputs are allocated here with torch unless passed in.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -37,6 +39,9 @@ SPLIT_SHIFT = 8
 TILE_SHIFT = 16
 PATH_PERSISTENT = 0x8          # the persistent (cooperative) kernel
 PATH_CLUSTER = 0x10            # the cluster kernel (one thread-block cluster per 40 tokens)
+
+GATE_SIGMOID = 0x20            # norm step: the gate tensor holds logits
+WEIGHTS_SHARED = 0x40          # norm step: one row of stream weights for all tokens
 
 N_STREAMS = 4
 MIX = (2 + N_STREAMS) * N_STREAMS
@@ -66,6 +71,15 @@ SIGNATURES = {
     "mhc_step_scratch_bytes": (_SZ, [_I, _I]),
     "mhc_fused_step_backward": (_I, [_P] * 25 + [_I64, _I, _I, _I, _F, _F, _U, _P, _SZ, _P]),
     "mhc_backward_workspace_bytes": (_SZ, [_I64, _I, _I]),
+    "mhc_checkpoint_save": (_I, [_P] * 3 + [_I64, _I, _P]),
+    "mhc_checkpoint_load": (_I, [_P] * 3 + [_I64, _I, _P]),
+    "mhc_checkpoint_scale_bytes": (_SZ, [_I64, _I]),
+    "mhc_fused_step_backward_ckpt": (_I, [_P] * 26 + [_I64, _I, _I, _I, _F, _F, _U, _P, _SZ, _P]),
+    "mhc_backward_ckpt_workspace_bytes": (_SZ, [_I64, _I, _I]),
+    "mhc_norm_step": (_I, [_P] * 10 + [_I64, _I, _I, _F, _F, _U, _P]),
+    "mhc_norm_step_backward": (_I, [_P] * 18 + [_I64, _I, _I, _F, _F, _U, _P, _SZ, _P]),
+    "mhc_norm_step_backward_ckpt": (_I, [_P] * 20 + [_I64, _I, _I, _F, _F, _U, _P, _SZ, _P]),
+    "mhc_norm_step_backward_workspace_bytes": (_SZ, [_I64, _I, _I]),
     "mhc_fused_step_noalloc": (_I, [_P] * 15 + [_I64, _I, _I, _I, _F, _F, _U, _P]),
     "mhc_noalloc_scratch_bytes": (_SZ, []),
     "mhc_fused_step_host": (_I, [_P] * 15 + [_I64, _I, _I, _I, _F, _F, _U, _P, _SZ, _I64, _P]),
@@ -302,6 +316,185 @@ def fused_step_backward(X, F, Xp, mixes, pre_prev, post_prev, comb_prev, W, scal
         _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "mhc_fused_step_backward")
     return o
+
+
+# ---------------------------------------------------------------------------------------------
+# activation checkpoints and the norm step
+
+def _need_all(spec):
+    """Checks (tensor, dtype, shape, name) entries: type, device, contiguity and shape, all on the
+    current device. Entries whose tensor is None are left out."""
+    current = torch.cuda.current_device()
+    for t, dtype, shape, name in spec:
+        if t is None:
+            continue
+        _need(t, dtype, name)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device.index != current:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{current}")
+
+
+def _on(stream):
+    """Tensors made inside belong to `stream` (the current one if None): the caching allocator hands
+    their memory out again only behind the work queued there."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _fill(out, shapes, device):
+    """`out` with the missing ones of `shapes` ({name: (shape, dtype)}) allocated, the given ones
+    checked."""
+    o = dict(out or {})
+    _need_all([(o.get(k), dtype, shape, k) for k, (shape, dtype) in shapes.items()])
+    for k, (shape, dtype) in shapes.items():
+        if o.get(k) is None:
+            o[k] = torch.empty(shape, dtype=dtype, device=device)
+    return o
+
+
+def _scale_shape(shape):
+    return (*shape[:-1], -(-shape[-1] // MX_BLOCK))
+
+
+def checkpoint_save(x, out=None, stream=None):
+    """mhc_checkpoint_save: bf16 x [..., d] -> (codes uint8 [..., d], scales uint8 [..., ceil(d/32)]),
+    the MXFP8 checkpoint of its rows. `out` is a (codes, scales) pair to write to."""
+    _need_all([(x, torch.bfloat16, x.shape, "x")])
+    codes, scales = out if out is not None else (None, None)
+    with _on(stream):
+        o = _fill({"codes": codes, "scales": scales},
+                  {"codes": (x.shape, torch.uint8), "scales": (_scale_shape(x.shape), torch.uint8)}, x.device)
+    d = x.shape[-1]
+    _check(lib.mhc_checkpoint_save(_ptr(x), _ptr(o["codes"]), _ptr(o["scales"]), math.prod(x.shape[:-1]), d,
+                                   _stream(stream)), "mhc_checkpoint_save")
+    return o["codes"], o["scales"]
+
+
+def checkpoint_load(codes, scales, out=None, stream=None):
+    """mhc_checkpoint_load: the bf16 rows [..., d] that a checkpoint stands for."""
+    _need_all([(codes, torch.uint8, codes.shape, "codes"),
+               (scales, torch.uint8, _scale_shape(codes.shape), "scales")])
+    with _on(stream):
+        x = _fill({"x": out}, {"x": (codes.shape, torch.bfloat16)}, codes.device)["x"]
+    _check(lib.mhc_checkpoint_load(_ptr(codes), _ptr(scales), _ptr(x), math.prod(codes.shape[:-1]),
+                                   codes.shape[-1], _stream(stream)), "mhc_checkpoint_load")
+    return x
+
+
+def backward_ckpt_workspace_bytes(N: int, d: int, n: int = N_STREAMS) -> int:
+    return int(lib.mhc_backward_ckpt_workspace_bytes(N, n, d))
+
+
+def fused_step_backward_ckpt(X_codes, X_scale, F_codes, F_scale, mixes, pre_prev, post_prev, comb_prev, W,
+                             scale, base, gain, gXp, gy, gpre, gpost, gcomb, *, iters=20, hc_eps=1e-6,
+                             norm_eps=1e-6, flags=0, out=None, workspace=None, stream=None):
+    """mhc_fused_step_backward_ckpt: fused_step_backward from checkpoints of X and F
+    (checkpoint_save), without X'. Same returns."""
+    N, n, d = X_codes.shape
+    u8, bf, fp = torch.uint8, torch.bfloat16, torch.float32
+    _need_all([(X_codes, u8, (N, n, d), "X_codes"), (X_scale, u8, _scale_shape((N, n, d)), "X_scale"),
+               (F_codes, u8, (N, d), "F_codes"), (F_scale, u8, _scale_shape((N, d)), "F_scale"),
+               (mixes, fp, (N, MIX), "mixes"), (pre_prev, fp, (N, n), "pre_prev"),
+               (post_prev, fp, (N, n), "post_prev"), (comb_prev, fp, (N, n, n), "comb_prev"),
+               (W, fp, (MIX, n * d), "W"), (scale, fp, (3,), "scale"), (base, fp, (MIX,), "base"),
+               (gain, fp, (d,), "gain"), (gXp, bf, (N, n, d), "gXp"), (gy, bf, (N, d), "gy"),
+               (gpre, fp, (N, n), "gpre"), (gpost, fp, (N, n), "gpost"), (gcomb, fp, (N, n, n), "gcomb")])
+    with _on(stream):
+        o = _fill(out, {"gX": ((N, n, d), bf), "gF": ((N, d), bf), "gpre_prev": ((N, n), fp),
+                        "gpost_prev": ((N, n), fp), "gcomb_prev": ((N, n, n), fp), "gW": ((MIX, n * d), fp),
+                        "gbase": ((MIX,), fp), "gscale": ((3,), fp), "ggain": ((d,), fp)}, X_codes.device)
+        if workspace is None:
+            workspace = torch.empty(max(1, backward_ckpt_workspace_bytes(N, d, n)), dtype=u8,
+                                    device=X_codes.device)
+    rc = lib.mhc_fused_step_backward_ckpt(
+        _ptr(X_codes), _ptr(X_scale), _ptr(F_codes), _ptr(F_scale), _ptr(mixes), _ptr(pre_prev),
+        _ptr(post_prev), _ptr(comb_prev), _ptr(W), _ptr(scale), _ptr(base), _ptr(gain), _ptr(gXp), _ptr(gy),
+        _ptr(gpre), _ptr(gpost), _ptr(gcomb), _ptr(o["gX"]), _ptr(o["gF"]), _ptr(o["gpre_prev"]),
+        _ptr(o["gpost_prev"]), _ptr(o["gcomb_prev"]), _ptr(o["gW"]), _ptr(o["gbase"]), _ptr(o["gscale"]),
+        _ptr(o["ggain"]), N, n, d, iters, hc_eps, norm_eps, flags, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "mhc_fused_step_backward_ckpt")
+    return o
+
+
+def _norm_shapes(N, n, d, gain_post, gain_pre, gate, pre, post, comb, flags):
+    rows = () if flags & WEIGHTS_SHARED else (N,)
+    fp = torch.float32
+    return [(gate, torch.bfloat16, (N, d), "gate"), (pre, fp, (*rows, n), "pre"), (post, fp, (*rows, n), "post"),
+            (comb, fp, (*rows, n, n), "comb"), (gain_post, fp, (d,), "gain_post"), (gain_pre, fp, (d,), "gain_pre")]
+
+
+def norm_step(X, F, gain_post, gain_pre, *, gate=None, pre=None, post=None, comb=None, res_scale=1.0,
+              norm_eps=1e-6, flags=0, out=None, stream=None):
+    """mhc_norm_step: the norm after a block (gain_post; None for no such norm) with its gate and
+    residual scale, the residual streams X [N, n, d] (n = 1 or 4) under given weights, and the norm
+    before the next block (gain_pre). Returns dict with Xp, y."""
+    N, n, d = X.shape
+    bf = torch.bfloat16
+    _need_all([(X, bf, (N, n, d), "X"), (F, bf, (N, d), "F"),
+               *_norm_shapes(N, n, d, gain_post, gain_pre, gate, pre, post, comb, flags)])
+    with _on(stream):
+        o = _fill(out, {"Xp": ((N, n, d), bf), "y": ((N, d), bf)}, X.device)
+    rc = lib.mhc_norm_step(_ptr(X), _ptr(F), _ptr(gate), _ptr(pre), _ptr(post), _ptr(comb), _ptr(gain_post),
+                           _ptr(gain_pre), _ptr(o["Xp"]), _ptr(o["y"]), N, n, d, res_scale, norm_eps, flags,
+                           _stream(stream))
+    _check(rc, "mhc_norm_step")
+    return o
+
+
+def norm_step_backward_workspace_bytes(N: int, d: int, n: int = N_STREAMS) -> int:
+    return int(lib.mhc_norm_step_backward_workspace_bytes(N, n, d))
+
+
+def _norm_step_backward(call, where, saved, N, n, d, gXp, gy, gain_post, gain_pre, gate, pre, post, comb,
+                        res_scale, norm_eps, flags, out, workspace, stream):
+    bf, fp = torch.bfloat16, torch.float32
+    _need_all([*saved, (gXp, bf, (N, n, d), "gXp"), (gy, bf, (N, d), "gy"),
+               *_norm_shapes(N, n, d, gain_post, gain_pre, gate, pre, post, comb, flags)])
+    shapes = {"gX": ((N, n, d), bf), "gF": ((N, d), bf), "ggain_pre": ((d,), fp)}
+    if gain_post is not None:
+        shapes["ggain_post"] = ((d,), fp)
+    if gate is not None:
+        shapes["ggate"] = ((N, d), bf)
+    if pre is not None:
+        rows = () if flags & WEIGHTS_SHARED else (N,)
+        shapes.update(gpre=((*rows, n), fp), gpost=((*rows, n), fp), gcomb=((*rows, n, n), fp))
+    with _on(stream):
+        o = _fill(out, shapes, gXp.device)
+        if workspace is None:
+            workspace = torch.empty(max(1, norm_step_backward_workspace_bytes(N, d, n)), dtype=torch.uint8,
+                                    device=gXp.device)
+    rc = call(*[_ptr(t) for t, _, _, _ in saved], _ptr(gate), _ptr(pre), _ptr(post), _ptr(comb),
+              _ptr(gain_post), _ptr(gain_pre), _ptr(gXp), _ptr(gy), _ptr(o["gX"]), _ptr(o["gF"]),
+              _ptr(o.get("ggate")), _ptr(o.get("gpre")), _ptr(o.get("gpost")), _ptr(o.get("gcomb")),
+              _ptr(o.get("ggain_post")), _ptr(o["ggain_pre"]), N, n, d, res_scale, norm_eps, flags,
+              _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, where)
+    return o
+
+
+def norm_step_backward(X, F, gXp, gy, gain_post, gain_pre, *, gate=None, pre=None, post=None, comb=None,
+                       res_scale=1.0, norm_eps=1e-6, flags=0, out=None, workspace=None, stream=None):
+    """mhc_norm_step_backward: gradients of norm_step from gXp, gy (those of Xp and y). Returns dict
+    with gX, gF, ggain_pre, and ggate, ggain_post, gpre, gpost, gcomb for what norm_step was given."""
+    N, n, d = X.shape
+    saved = [(X, torch.bfloat16, (N, n, d), "X"), (F, torch.bfloat16, (N, d), "F")]
+    return _norm_step_backward(lib.mhc_norm_step_backward, "mhc_norm_step_backward", saved, N, n, d, gXp, gy,
+                               gain_post, gain_pre, gate, pre, post, comb, res_scale, norm_eps, flags, out,
+                               workspace, stream)
+
+
+def norm_step_backward_ckpt(X_codes, X_scale, F_codes, F_scale, gXp, gy, gain_post, gain_pre, *, gate=None,
+                            pre=None, post=None, comb=None, res_scale=1.0, norm_eps=1e-6, flags=0, out=None,
+                            workspace=None, stream=None):
+    """mhc_norm_step_backward_ckpt: norm_step_backward from checkpoints of X and F (checkpoint_save)."""
+    N, n, d = X_codes.shape
+    u8 = torch.uint8
+    saved = [(X_codes, u8, (N, n, d), "X_codes"), (X_scale, u8, _scale_shape((N, n, d)), "X_scale"),
+             (F_codes, u8, (N, d), "F_codes"), (F_scale, u8, _scale_shape((N, d)), "F_scale")]
+    return _norm_step_backward(lib.mhc_norm_step_backward_ckpt, "mhc_norm_step_backward_ckpt", saved, N, n, d,
+                               gXp, gy, gain_post, gain_pre, gate, pre, post, comb, res_scale, norm_eps, flags,
+                               out, workspace, stream)
 
 
 def fused_step_noalloc(X, F, pre_prev, post_prev, comb_prev, W, scale, base, gain, *, iters=20,
