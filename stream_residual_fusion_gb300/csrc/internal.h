@@ -213,6 +213,7 @@ struct NormArgs {
   float* ggain_post;
   float* ggain_pre;
   float* partial;           // norm_backward_rows(N) rows of norm_partial_floats(d)
+  unsigned* status;         // the library's status word
   int64_t N;
   int n;
   int d;

@@ -64,7 +64,14 @@ __device__ __forceinline__ C8 gain8(const float* g, int c) {
   return C8{{f2{a.x, a.y}, f2{a.z, a.w}, f2{b.x, b.y}, f2{b.z, b.w}}};
 }
 __device__ __forceinline__ f2 both(float v) { return f2{v, v}; }
-__device__ __forceinline__ float sigmoid_n(float z) { return 1.0f / (1.0f + expf(-z)); }
+// 1 / (1 + 2^(-z log2 e)) on the special-function unit: the rounded exponent puts it off by about
+// |z| 2^-24 of itself besides the 2^-22 of the two approximations; 0 and 1 at the infinities.
+__device__ __forceinline__ float sigmoid_n(float z) {
+  float e, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
 
 // Row `row` of a tensor, chunk c of 8 features: bf16, or MXFP8 codes and scales.
 template <bool CK>
@@ -321,6 +328,618 @@ __global__ void __launch_bounds__(NT) norm_step_backward_kernel(const NormArgs P
   if ((P.flags & FLAG_WEIGHTS_SHARED) && threadIdx.x < NSUM - 1) part_w[threadIdx.x] = shared_sum;
 }
 
+// ---------------------------------------------------------------------------------------------
+// The staged kernels: blocks walk the tokens, a producer warp copies each token's rows into shared
+// memory ahead of the consumers (bulk copies of whole rows), and the consumers read a row there as
+// often as they need it, so that HBM is read once. Thread i owns the chunks i, i + T, ... (CH of them)
+// of every token, so the gains' gradients gather in its registers.
+
+constexpr uint64_t NORM_WAIT_NS = 2000000000ull;   // 2 s
+constexpr int SMAX_WARPS = 12;                     // consumer warps of a block, at most
+constexpr int SMAX_STAGES = 4;
+
+// A token's rows in a stage: byte offsets, the stage's size and that of X, which has stages of its own
+// (multiples of 128).
+struct Stage {
+  int f, gate, gxp, gy, w, bytes, xbytes;   // F at 0
+};
+template <int NS, bool CK, bool BACK>
+__host__ __device__ constexpr Stage stage_of(int d) {
+  Stage s{};
+  const int e = CK ? 1 : 2;
+  s.gate = d * e;
+  s.gxp = s.gate + 2 * d;
+  s.gy = s.gxp + (BACK ? NS * 2 * d : 0);
+  s.w = s.gy + (BACK ? 2 * d : 0);
+  s.bytes = (s.w + (NS == 4 ? 96 : 0) + 127) / 128 * 128;
+  s.xbytes = (NS * d * e + 127) / 128 * 128;
+  return s;
+}
+// Stages of a block: of a token's rows, and of its X.
+struct Ring {
+  int rows, x;
+};
+struct Barriers {
+  uint64_t full[SMAX_STAGES], empty[SMAX_STAGES], xfull[SMAX_STAGES], xempty[SMAX_STAGES];
+};
+
+// Lane l gets the warp's total of value l % V.
+template <int V>
+__device__ __forceinline__ float warp_sums(float (&v)[V]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = V / 2; h >= 1; h /= 2) {
+    const bool up = (lane & h) != 0;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float send = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, h);
+    }
+  }
+#pragma unroll
+  for (int o = V; o < 32; o *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+// The block's totals from each warp's V sums (scratch [warps][V]; one barrier of the `nthreads`
+// consumers): lane l of every warp gets that of value l % V. The next use of `scratch` has to come
+// after another barrier.
+template <int V>
+__device__ __forceinline__ float group_sums(float (&v)[V], float* scratch, int warps, int nthreads) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float mine = warp_sums<V>(v);
+  if (lane < V) scratch[warp * V + lane] = mine;
+  named_bar_sync(1, nthreads);
+  float t = 0.f;
+  for (int w = 0; w < warps; ++w) t += scratch[w * V + (lane & (V - 1))];
+  return t;
+}
+__device__ __forceinline__ float lane_value(float v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
+
+__device__ __forceinline__ C8 shared8(const uint8_t* p, int c) {
+  return unpack8(*reinterpret_cast<const uint4*>(p + 16 * c));
+}
+// Chunk c of a checkpointed row in shared memory under scale code e.
+__device__ __forceinline__ C8 shared8_codes(const uint8_t* p, int c, uint32_t e) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p + 8 * c);
+  const f2 s = both(scale_value(e));
+  return C8{{decode2(v.x, s), decode2(v.x >> 16, s), decode2(v.y, s), decode2(v.y >> 16, s)}};
+}
+// The stream weights as pairs.
+template <int NS>
+struct Weights2 {
+  f2 p[NS], u[NS], cc[NS][NS];
+};
+template <int NS>
+__device__ __forceinline__ Weights2<NS> stage_weights(const uint8_t* w, bool row_dest) {
+  Weights2<NS> o;
+  const float* f = reinterpret_cast<const float*>(w);
+#pragma unroll
+  for (int k = 0; k < NS; ++k) {
+    o.p[k] = both(f[k]);
+    o.u[k] = both(f[NS + k]);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) o.cc[j][k] = both(f[2 * NS + (row_dest ? k * NS + j : j * NS + k)]);
+  }
+  return o;
+}
+__device__ __forceinline__ Weights2<1> scalar_weights(const NormArgs& P, int64_t t) {
+  const Weights<1> w = load_weights<1>(P, t);
+  return Weights2<1>{{both(w.p[0])}, {both(w.u[0])}, {{both(w.cc[0][0])}}};
+}
+
+__device__ __forceinline__ void init_barriers(Barriers& B, const Ring& R, int warps) {
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < R.rows; ++b) {
+      mbar_init(&B.full[b], 1);
+      mbar_init(&B.empty[b], warps);
+    }
+    for (int b = 0; b < R.x; ++b) {
+      mbar_init(&B.xfull[b], 1);
+      mbar_init(&B.xempty[b], warps);
+    }
+    fence_mbar_init();
+  }
+  block_sync();
+}
+
+// The producer's loop over this block's tokens (one thread).
+template <int NS, bool CK, bool BACK>
+__device__ __forceinline__ bool produce(const NormArgs& P, uint8_t* sm, Barriers& B, const Ring& R) {
+  const Stage S = stage_of<NS, CK, BACK>(P.d);
+  const uint64_t pol = policy_evict_first();
+  const uint32_t row = 2u * P.d, saved = (CK ? 1u : 2u) * P.d;
+  const uint32_t bytes = saved + (P.gate ? row : 0u) + (BACK ? (NS + 1) * row : 0u) + (NS == 4 ? 96u : 0u);
+  uint8_t* xs = sm + R.rows * S.bytes;
+  bool late = false;
+  auto free_of = [&](uint64_t* empty, int i, int stages) {
+    if (i >= stages && !mbar_wait(&empty[i % stages], ((i / stages) - 1) & 1, late ? 0ull : NORM_WAIT_NS)) late = true;
+  };
+  int i = 0;
+  for (int64_t t = blockIdx.x; t < P.N; t += gridDim.x, ++i) {
+    const int b = i % R.rows, x = i % R.x;
+    auto at = [&](const void* p, int64_t n) { return static_cast<const uint8_t*>(p) + t * n; };
+    free_of(B.empty, i, R.rows);
+    uint8_t* st = sm + b * S.bytes;
+    mbar_arrive_expect_tx(&B.full[b], bytes);
+    bulk_load_hint(st, at(P.F, saved), saved, &B.full[b], pol);
+    if (P.gate) bulk_load_hint(st + S.gate, at(P.gate, row), row, &B.full[b], pol);
+    if (BACK) {
+      bulk_load_hint(st + S.gy, at(P.gy, row), row, &B.full[b], pol);
+      bulk_load_hint(st + S.gxp, at(P.gXp, static_cast<int64_t>(NS) * row), NS * row, &B.full[b], pol);
+    }
+    if (NS == 4) {
+      const int64_t wt = (P.flags & FLAG_WEIGHTS_SHARED) ? 0 : t;
+      bulk_load_hint(st + S.w, P.pre + wt * 4, 16, &B.full[b], pol);
+      bulk_load_hint(st + S.w + 16, P.post + wt * 4, 16, &B.full[b], pol);
+      bulk_load_hint(st + S.w + 32, P.comb + wt * 16, 64, &B.full[b], pol);
+    }
+    free_of(B.xempty, i, R.x);
+    mbar_arrive_expect_tx(&B.xfull[x], NS * saved);
+    bulk_load_hint(xs + x * S.xbytes, at(P.X, static_cast<int64_t>(NS) * saved), NS * saved, &B.xfull[x], pol);
+  }
+  return late;
+}
+
+// Gate and gain of one chunk: s a, the gain, and the gate's derivative.
+__device__ __forceinline__ void gate_gain(const NormArgs& P, const uint8_t* gate, int c, C8& sa, C8& da, C8& g) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sa.v[i] = both(P.res_scale);
+    da.v[i] = g.v[i] = both(1.f);
+  }
+  if (P.gain_post) g = gain8(P.gain_post, c);
+  if (!P.gate) return;
+  C8 a = shared8(gate, c);
+  if (P.flags & FLAG_GATE_SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a.v[i] = f2{sigmoid_n(a.v[i].x), sigmoid_n(a.v[i].y)};
+      da.v[i] = f2{a.v[i].x * (1.f - a.v[i].x), a.v[i].y * (1.f - a.v[i].y)};
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sa.v[i] = mul2(both(P.res_scale), a.v[i]);
+}
+
+__device__ __forceinline__ float inv_rms(float sum, float d, float eps) {
+  return __frsqrt_rn(__fdiv_rn(sum, d) + eps);
+}
+
+template <int NS, int CH>
+__global__ void __launch_bounds__((SMAX_WARPS + 1) * 32, 1) norm_step_staged(const NormArgs P, Ring R) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ Barriers B;
+  __shared__ float scratch[2][SMAX_WARPS * 2];
+  const Stage S = stage_of<NS, false, false>(P.d);
+  const int warps = blockDim.x / 32 - 1, T = warps * 32, lane = threadIdx.x & 31;
+  const int chunks = P.d / 8;
+  const float fd = static_cast<float>(P.d);
+  bool late = false;
+  init_barriers(B, R, warps);
+  if (static_cast<int>(threadIdx.x) >= T) {
+    if (lane == 0) late = produce<NS, false, false>(P, sm, B, R);
+  } else {
+    auto wait = [&](uint64_t* full, int i, int stages) {
+      if (!mbar_wait(&full[i % stages], (i / stages) & 1, late ? 0ull : NORM_WAIT_NS)) late = true;
+    };
+    auto sum_f = [&](const uint8_t* st) {
+      f2 s{0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < CH; ++q) {
+        const int c = static_cast<int>(threadIdx.x) + q * T;
+        if (c >= chunks) break;
+        const C8 f = shared8(st, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s = fma2(f.v[i], f.v[i], s);
+      }
+      return s.x + s.y;
+    };
+    // one barrier a token: the sum of yh^2 and the next token's of F^2 go together
+    float r = 1.f;
+    if (P.gain_post && blockIdx.x < P.N) {
+      wait(B.full, 0, R.rows);
+      float v[2] = {0.f, sum_f(sm)};
+      r = inv_rms(lane_value(group_sums<2>(v, scratch[1], warps, T), 1), fd, P.eps);
+    }
+    int n = 0;
+    for (int64_t t = blockIdx.x; t < P.N; t += gridDim.x, ++n) {
+      const uint8_t* st = sm + (n % R.rows) * S.bytes;
+      const uint8_t* xt = sm + R.rows * S.bytes + (n % R.x) * S.xbytes;
+      wait(B.full, n, R.rows);
+      wait(B.xfull, n, R.x);
+      Weights2<NS> w;
+      if constexpr (NS == 4) {
+        w = stage_weights<NS>(st + S.w, (P.flags & 1u) != 0);
+      } else {
+        w = scalar_weights(P, t);
+      }
+      C8 yh[CH];
+      f2 s{0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < CH; ++q) {
+        const int c = static_cast<int>(threadIdx.x) + q * T;
+        if (c >= chunks) break;
+        C8 x[NS], sa, da, g, xp[NS];
+        const C8 f = shared8(st, c);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) x[j] = shared8(xt + j * 2 * P.d, c);
+        gate_gain(P, st + S.gate, c, sa, da, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 z = mul2(mul2(mul2(sa.v[i], g.v[i]), f.v[i]), both(r));
+          f2 y{0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < NS; ++k) {
+            f2 v = mul2(w.u[k], z);
+#pragma unroll
+            for (int j = 0; j < NS; ++j) v = fma2(w.cc[j][k], x[j].v[i], v);
+            xp[k].v[i] = v;
+            y = fma2(w.p[k], v, y);
+          }
+          s = fma2(y, y, s);
+          yh[q].v[i] = y;
+        }
+#pragma unroll
+        for (int k = 0; k < NS; ++k) reinterpret_cast<uint4*>(P.X_out)[(t * NS + k) * chunks + c] = pack8(xp[k]);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&B.empty[n % R.rows]);
+        mbar_arrive(&B.xempty[n % R.x]);
+      }
+      float v[2] = {s.x + s.y, 0.f};
+      if (P.gain_post && t + gridDim.x < P.N) {
+        wait(B.full, n + 1, R.rows);
+        v[1] = sum_f(sm + ((n + 1) % R.rows) * S.bytes);
+      }
+      const float tot = group_sums<2>(v, scratch[n & 1], warps, T);
+      const float ry = inv_rms(lane_value(tot, 0), fd, P.eps);
+      if (P.gain_post) r = inv_rms(lane_value(tot, 1), fd, P.eps);
+#pragma unroll
+      for (int q = 0; q < CH; ++q) {
+        const int c = static_cast<int>(threadIdx.x) + q * T;
+        if (c >= chunks) break;
+        const C8 g = gain8(P.gain_pre, c);
+        C8 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o.v[i] = mul2(g.v[i], mul2(yh[q].v[i], both(ry)));
+        reinterpret_cast<uint4*>(P.y)[t * chunks + c] = pack8(o);
+      }
+    }
+  }
+  if (late) atomicOr(P.status, STATUS_TIMEOUT);
+}
+
+// The backward works in units of 4 features (8 bytes of a bf16 row), UN of them a thread: what a thread
+// holds of a token's rows at a time has to leave room for its weights and sums.
+template <bool CK>
+struct Row4 {
+  uint32_t w[CK ? 1 : 2];
+  float s;
+  __device__ __forceinline__ f2 at(int i) const {
+    if constexpr (CK) return decode2(w[0] >> (16 * i), both(s));
+    else return bf2_to_f2(w[i]);
+  }
+};
+__device__ __forceinline__ Row4<false> row4(const uint8_t* p, int u) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p + 8 * u);
+  return Row4<false>{{v.x, v.y}, 1.f};
+}
+template <bool CK>
+__device__ __forceinline__ Row4<CK> saved4(const uint8_t* p, int u, uint32_t code) {
+  if constexpr (CK) return Row4<true>{{*reinterpret_cast<const uint32_t*>(p + 4 * u)}, scale_value(code & 0xffu)};
+  else return row4(p, u);
+}
+__device__ __forceinline__ void store4(void* p, int64_t u, const uint32_t (&w)[2]) {
+  reinterpret_cast<uint2*>(p)[u] = make_uint2(w[0], w[1]);
+}
+struct C4 {
+  f2 v[2];
+};
+__device__ __forceinline__ C4 gain4(const float* g, int u) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(g) + u);
+  return C4{{f2{a.x, a.y}, f2{a.z, a.w}}};
+}
+
+// Threads of the backward's blocks: 11 consumer warps and the producer, 168 registers a thread (80 with one
+// stream and few features, for two blocks a multiprocessor).
+constexpr int SBACK_THREADS = 384;
+
+// Two passes over a token. The first takes the sums over the width that everything else needs: with
+// gg = gpre gy, y = yh, alpha = p.u and beta_j = sum_k C_jk p_k (y = alpha z + sum_j beta_j x_j),
+//   y.y, gg.y (r_y and tau), gg.z, gg.x_j, y.z, y.x_j, gXp_k.z, gXp_k.x_j.
+// The weights' gradients are combinations of them (gyh = r_y gg - tau y and G_k = gXp_k + p_k gyh):
+//   e_z = gyh.z, e_j = gyh.x_j, gp_k = u_k e_z + sum_j C_jk e_j, gu_k = gXp_k.z + p_k e_z, gC_jk = gXp_k.x_j + p_k e_j.
+// The second forms gX_j = sum_k C_jk gXp_k + beta_j gyh, q = sum_k u_k gXp_k + alpha gyh and what follows from
+// q, with no X; gF waits for the sum S.
+template <int NS, bool CK, int UN>
+__global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
+    norm_step_backward_staged(const NormArgs P, const Ring R) {
+  constexpr int IE = 2, IG = 4 + 2 * NS;  // where gg.z, gg.x_j and gXp_k.z, gXp_k.x_j begin
+  constexpr int V = NS == 4 ? 32 : 8;
+  static_assert(IG + NS + NS * NS == V, "sums");
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ Barriers B;
+  __shared__ float scratch1[SMAX_WARPS], scratch2[2][SMAX_WARPS * V], scratch3[SMAX_WARPS * 2];
+  const Stage S = stage_of<NS, CK, true>(P.d);
+  const int warps = blockDim.x / 32 - 1, T = warps * 32, lane = threadIdx.x & 31;
+  const int units = P.d / 4, blocks = (P.d + MX_BLOCK - 1) / MX_BLOCK;
+  const int srow = P.d * (CK ? 1 : 2);   // bytes of a saved row
+  const float fd = static_cast<float>(P.d);
+  const bool row_dest = (P.flags & 1u) != 0, shared = (P.flags & FLAG_WEIGHTS_SHARED) != 0;
+  const bool sigmoid = (P.flags & FLAG_GATE_SIGMOID) != 0;
+  bool late = false;
+  init_barriers(B, R, warps);
+  if (static_cast<int>(threadIdx.x) >= T) {
+    if (lane == 0) late = produce<NS, CK, true>(P, sm, B, R);
+  } else {
+    auto wait = [&](uint64_t* full, int i, int stages) {
+      if (!mbar_wait(&full[i % stages], (i / stages) & 1, late ? 0ull : NORM_WAIT_NS)) late = true;
+    };
+    // scale codes of a token's units (X's streams, low byte first; F), read a token ahead
+    struct Codes {
+      uint32_t x, f;
+    };
+    auto scales = [&](int64_t t, Codes (&o)[UN]) {
+      if (!CK || t >= P.N) return;
+#pragma unroll
+      for (int q = 0; q < UN; ++q) {
+        const int u = static_cast<int>(threadIdx.x) + q * T;
+        if (u >= units) break;
+        o[q].x = 0;
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+          o[q].x |= static_cast<uint32_t>(__ldg(P.X_scale + (t * NS + j) * blocks + u / 8)) << (8 * j);
+        o[q].f = __ldg(P.F_scale + t * blocks + u / 8);
+      }
+    };
+    auto sum_f = [&](const uint8_t* st, const Codes (&s)[UN]) {
+      f2 a{0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < UN; ++q) {
+        const int u = static_cast<int>(threadIdx.x) + q * T;
+        if (u >= units) break;
+        const Row4<CK> f = saved4<CK>(st, u, s[q].f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) a = fma2(f.at(i), f.at(i), a);
+      }
+      return a.x + a.y;
+    };
+    // s a of a unit, and the gate's derivative
+    auto gate_of = [&](const uint8_t* st, int u, C4& sa, C4& da) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sa.v[i] = both(P.res_scale);
+        da.v[i] = both(1.f);
+      }
+      if (!P.gate) return;
+      const Row4<false> a = row4(st + S.gate, u);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f2 v = a.at(i);
+        if (sigmoid) {
+          v = f2{sigmoid_n(v.x), sigmoid_n(v.y)};
+          da.v[i] = f2{v.x * (1.f - v.x), v.y * (1.f - v.y)};
+        }
+        sa.v[i] = mul2(both(P.res_scale), v);
+      }
+    };
+    const C4 ones{{both(1.f), both(1.f)}};
+    C4 acc_pre[UN], acc_post[UN];
+#pragma unroll
+    for (int q = 0; q < UN; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc_pre[q].v[i] = acc_post[q].v[i] = f2{0.f, 0.f};
+    float total_gp = 0.f, total_w = 0.f;   // shared weights: this lane's value over the tokens
+    Codes sc[UN], sn[UN];
+    scales(blockIdx.x, sc);
+    // With more than one stage the sum of the next token's F^2 goes with this one's last sum.
+    const bool ahead = R.rows > 1;
+    float r = 1.f;
+    int n = 0;
+    for (int64_t t = blockIdx.x; t < P.N; t += gridDim.x, ++n) {
+      const uint8_t* st = sm + (n % R.rows) * S.bytes;
+      const uint8_t* xt = sm + R.rows * S.bytes + (n % R.x) * S.xbytes;
+      wait(B.full, n, R.rows);
+      if (P.gain_post && (n == 0 || !ahead)) {
+        float v[1] = {sum_f(st, sc)};
+        r = inv_rms(group_sums<1>(v, scratch1, warps, T), fd, P.eps);
+      }
+      scales(t + gridDim.x, sn);
+      Weights<NS> w;
+      if constexpr (NS == 4) {
+        const float* wf = reinterpret_cast<const float*>(st + S.w);
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+          w.p[k] = wf[k];
+          w.u[k] = wf[NS + k];
+#pragma unroll
+          for (int j = 0; j < NS; ++j) w.cc[j][k] = wf[2 * NS + (row_dest ? k * NS + j : j * NS + k)];
+        }
+      } else {
+        w = load_weights<NS>(P, t);
+      }
+      float alpha = 0.f, beta[NS];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        alpha = fmaf(w.p[j], w.u[j], alpha);
+        beta[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < NS; ++k) beta[j] = fmaf(w.cc[j][k], w.p[k], beta[j]);
+      }
+      wait(B.xfull, n, R.x);
+      C4 yh[UN];
+      float tot;
+      {
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.f;
+        auto dot = [&](int i, f2 a, f2 b) { v[i] = fmaf(a.x, b.x, fmaf(a.y, b.y, v[i])); };
+#pragma unroll
+        for (int q = 0; q < UN; ++q) {
+          const int u = static_cast<int>(threadIdx.x) + q * T;
+          if (u >= units) break;
+          Row4<CK> x[NS];
+          Row4<false> gxp[NS];
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            x[j] = saved4<CK>(xt + j * srow, u, sc[q].x >> (8 * j));
+            gxp[j] = row4(st + S.gxp + j * 2 * P.d, u);
+          }
+          const Row4<CK> f = saved4<CK>(st, u, sc[q].f);
+          const Row4<false> gy = row4(st + S.gy, u);
+          C4 sa, da;
+          gate_of(st, u, sa, da);
+          const C4 g = P.gain_post ? gain4(P.gain_post, u) : ones, gn = gain4(P.gain_pre, u);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const f2 z = mul2(mul2(sa.v[i], mul2(f.at(i), both(r))), g.v[i]);
+            f2 xi[NS], gi[NS], y = mul2(both(alpha), z);
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              xi[j] = x[j].at(i);
+              gi[j] = gxp[j].at(i);
+              y = fma2(both(beta[j]), xi[j], y);
+            }
+            const f2 gg = mul2(gn.v[i], gy.at(i));
+            dot(0, y, y);
+            dot(1, gg, y);
+            dot(IE, gg, z);
+            dot(IE + NS + 1, y, z);
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              dot(IE + 1 + j, gg, xi[j]);
+              dot(IE + NS + 2 + j, y, xi[j]);
+              dot(IG + j, gi[j], z);
+#pragma unroll
+              for (int k = 0; k < NS; ++k) dot(IG + NS + j * NS + k, gi[k], xi[j]);
+            }
+            yh[q].v[i] = y;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.xempty[n % R.x]);
+        tot = group_sums<V>(v, scratch2[n & 1], warps, T);
+      }
+      const float ry = inv_rms(lane_value(tot, 0), fd, P.eps);
+      const float tau = ry * ry * ry * lane_value(tot, 1) / fd;
+      if (P.pre && threadIdx.x < 32) {
+        const float e = ry * tot - tau * __shfl_down_sync(0xffffffffu, tot, NS + 1);   // lanes IE ..: e_z, e_j
+        const float ez = lane_value(e, IE);
+        float ej[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) ej[j] = lane_value(e, IE + 1 + j);
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+          float gp = w.u[k] * ez;
+#pragma unroll
+          for (int j = 0; j < NS; ++j) gp = fmaf(w.cc[j][k], ej[j], gp);
+          if (lane == k) {
+            if (shared) total_gp += gp;
+            else P.gpre[t * NS + k] = gp;
+          }
+          if (lane == IG + k) {
+            const float gu = fmaf(w.p[k], ez, tot);
+            if (shared) total_w += gu;
+            else P.gpost[t * NS + k] = gu;
+          }
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            if (lane == IG + NS + j * NS + k) {
+              const float gc = fmaf(w.p[k], ej[j], tot);
+              if (shared) total_w += gc;
+              else P.gcomb[t * NS * NS + (row_dest ? k * NS + j : j * NS + k)] = gc;
+            }
+          }
+        }
+      }
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < UN; ++q) {
+        const int u = static_cast<int>(threadIdx.x) + q * T;
+        if (u >= units) break;
+        Row4<false> gxp[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) gxp[j] = row4(st + S.gxp + j * 2 * P.d, u);
+        const Row4<CK> f = saved4<CK>(st, u, sc[q].f);
+        const Row4<false> gy = row4(st + S.gy, u);
+        C4 sa, da;
+        gate_of(st, u, sa, da);
+        const C4 g = P.gain_post ? gain4(P.gain_post, u) : ones, gn = gain4(P.gain_pre, u);
+        uint32_t gx[NS][2], gg[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const f2 y = yh[q].v[i], ryg = mul2(gy.at(i), both(ry));
+          const f2 gyh = fma2(ryg, gn.v[i], mul2(both(-tau), y));
+          acc_pre[q].v[i] = fma2(ryg, y, acc_pre[q].v[i]);
+          const f2 fi = f.at(i), fr = mul2(fi, both(r)), safr = mul2(sa.v[i], fr);
+          f2 gi[NS], qq = mul2(both(alpha), gyh);
+#pragma unroll
+          for (int k = 0; k < NS; ++k) {
+            gi[k] = gxp[k].at(i);
+            qq = fma2(both(w.u[k]), gi[k], qq);
+          }
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            f2 v = mul2(both(beta[j]), gyh);
+#pragma unroll
+            for (int k = 0; k < NS; ++k) v = fma2(both(w.cc[j][k]), gi[k], v);
+            gx[j][i] = f2_to_bf2(v);
+          }
+          const f2 hq = mul2(mul2(sa.v[i], g.v[i]), qq);
+          s = fmaf(hq.x, fi.x, fmaf(hq.y, fi.y, s));
+          acc_post[q].v[i] = fma2(safr, qq, acc_post[q].v[i]);
+          gg[i] = f2_to_bf2(mul2(mul2(mul2(both(P.res_scale), g.v[i]), mul2(fr, qq)), da.v[i]));
+          yh[q].v[i] = hq;   // yh is done with: h q waits here for S
+        }
+#pragma unroll
+        for (int j = 0; j < NS; ++j) store4(P.gX, (t * NS + j) * units + u, gx[j]);
+        if (P.gate) store4(P.ggate, t * units + u, gg);
+      }
+      float v[2] = {s, 0.f};
+      if (P.gain_post && ahead && t + gridDim.x < P.N) {
+        wait(B.full, n + 1, R.rows);
+        v[1] = sum_f(sm + ((n + 1) % R.rows) * S.bytes, sn);
+      }
+      const float tot3 = P.gain_post ? group_sums<2>(v, scratch3, warps, T) : 0.f;
+      const float cf = P.gain_post ? r * r * r * lane_value(tot3, 0) / fd : 0.f;
+#pragma unroll
+      for (int q = 0; q < UN; ++q) {
+        const int u = static_cast<int>(threadIdx.x) + q * T;
+        if (u >= units) break;
+        const Row4<CK> f = saved4<CK>(st, u, sc[q].f);
+        uint32_t o[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) o[i] = f2_to_bf2(fma2(both(r), yh[q].v[i], mul2(both(-cf), f.at(i))));
+        store4(P.gF, t * units + u, o);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.empty[n % R.rows]);
+      if (P.gain_post) r = inv_rms(lane_value(tot3, 1), fd, P.eps);
+      if constexpr (CK) {
+#pragma unroll
+        for (int q = 0; q < UN; ++q) sc[q] = sn[q];
+      }
+    }
+    float* part = P.partial + blockIdx.x * static_cast<int64_t>(norm_partial_floats(P.d));
+#pragma unroll
+    for (int q = 0; q < UN; ++q) {
+      const int u = static_cast<int>(threadIdx.x) + q * T;
+      if (u >= units) break;
+      auto put = [&](float* p, const C4& a) {
+        reinterpret_cast<float4*>(p)[u] = make_float4(a.v[0].x, a.v[0].y, a.v[1].x, a.v[1].y);
+      };
+      put(part, acc_pre[q]);
+      put(part + P.d, acc_post[q]);
+    }
+    if (shared && P.pre && threadIdx.x < 32) {
+      if (lane < NS) part[2 * P.d + lane] = total_gp;
+      if (lane >= IG && lane < V) part[2 * P.d + NS + lane - IG] = total_w;
+    }
+  }
+  if (late) atomicOr(P.status, STATUS_TIMEOUT);
+}
+
 // Sums of the blocks' partial rows, in the blocks' order: 32 columns a block, 8 threads a column.
 __global__ void __launch_bounds__(256) norm_reduce_kernel(const NormArgs P, int rows) {
   __shared__ float red[8][33];
@@ -353,13 +972,21 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const NormArgs P, int 
   }
 }
 
-int norm_sms() {
-  int dev = 0, sms = 0;
+struct Device {
+  int sms, smem;   // multiprocessors, shared memory a block may have
+};
+Device norm_device() {
+  int dev = 0;
+  Device v{0, 0};
   if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
+      cudaDeviceGetAttribute(&v.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&v.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
+    return Device{0, 0};
+  return v;
 }
+
+// Blocks of the backward, and so rows of partial sums: at most this many per multiprocessor.
+constexpr int NORM_BACK_BLOCKS = 4;
 
 template <typename K>
 cudaError_t launch_rows(K kernel, const NormArgs& a, int64_t grid, cudaStream_t stream) {
@@ -372,30 +999,112 @@ cudaError_t launch_rows(K kernel, const NormArgs& a, int64_t grid, cudaStream_t 
   return cudaGetLastError();
 }
 
+// Consumer threads of the staged kernels for `items` of a row, `each` a thread; 0 if there are over `most`.
+int staged_threads(int items, int each, int most) {
+  const int t = ((items + each - 1) / each + 31) / 32 * 32;
+  return t <= most ? t : 0;
+}
+
+// Shared memory left free for the L1 cache where that can be: the gains, read for every token.
+int l1_room(int d) { return 12 * d; }
+
+// Launches a staged kernel (`kernel`, its stage sizes S) where a stage fits at all. cap: blocks per
+// multiprocessor. *ran: the launched blocks, 0 if the kernel does not take this size.
+template <typename K>
+cudaError_t launch_staged(K kernel, const NormArgs& a, int threads, const Stage& S, const Device& dev, int cap,
+                          int* ran, cudaStream_t stream) {
+  *ran = 0;
+  constexpr int kStatic = 4096;   // the kernels' static shared memory and the system's share of it, at most
+  const int one = S.bytes + S.xbytes, room = dev.smem - kStatic;
+  if (threads == 0 || one > room) return cudaSuccess;
+  // several blocks a multiprocessor where two stages of each fit, else one block with two stages of the
+  // rows and one of X, else one of each
+  const int block = threads + 32;
+  int per = std::max(1, std::min({cap, (room - l1_room(a.d)) / (2 * one + kStatic), 2048 / block}));
+  cudaError_t e;
+  Ring R{1, 1};
+  if (per > 1) {
+    int fit = 0;
+    R = Ring{2, 2};
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * one);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, block, 2 * one);
+    if (e != cudaSuccess) return e;
+    per = std::max(1, std::min(per, fit));
+  }
+  const int space = room / per - (per > 1 ? kStatic : 0) - l1_room(a.d) / per;
+  if (2 * one <= space) {
+    R.rows = R.x = std::min(SMAX_STAGES, space / one);
+  } else if (2 * S.bytes + S.xbytes <= room) {
+    R = Ring{2, 1};
+  }
+  const int smem = R.rows * S.bytes + R.x * S.xbytes;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  *ran = static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(dev.sms) * per));
+  kernel<<<*ran, block, smem, stream>>>(a, R);
+  return cudaGetLastError();
+}
+
+template <int NS>
+cudaError_t forward_of(const NormArgs& a, const Device& dev, cudaStream_t stream) {
+  const Stage stage = stage_of<NS, false, false>(a.d);
+  const int most = SMAX_WARPS * 32;
+  int ran = 0;
+  cudaError_t e;
+  if (const int t = staged_threads(a.d / 8, 1, most))
+    e = launch_staged(norm_step_staged<NS, 1>, a, t, stage, dev, 8, &ran, stream);
+  else if (const int t2 = staged_threads(a.d / 8, 2, most))
+    e = launch_staged(norm_step_staged<NS, 2>, a, t2, stage, dev, 8, &ran, stream);
+  else
+    e = launch_staged(norm_step_staged<NS, 4>, a, staged_threads(a.d / 8, 4, most), stage, dev, 8, &ran, stream);
+  if (e != cudaSuccess || ran > 0) return e;
+  return launch_rows(norm_step_kernel<NS>, a, std::min<int64_t>(a.N, static_cast<int64_t>(dev.sms) * 8), stream);
+}
+
+template <int NS, bool CK>
+cudaError_t backward_of(const NormArgs& a, const Device& dev, int* rows, cudaStream_t stream) {
+  *rows = 0;
+  // bulk copies of a row of codes take whole 16-byte units
+  if (!CK || a.d % 16 == 0) {
+    const Stage stage = stage_of<NS, CK, true>(a.d);
+    const int most = SBACK_THREADS - 32;
+    cudaError_t e;
+    if (const int t = staged_threads(a.d / 4, 2, most))
+      e = launch_staged(norm_step_backward_staged<NS, CK, 2>, a, t, stage, dev, NORM_BACK_BLOCKS, rows, stream);
+    else if (const int t4 = staged_threads(a.d / 4, 4, most))
+      e = launch_staged(norm_step_backward_staged<NS, CK, 4>, a, t4, stage, dev, NORM_BACK_BLOCKS, rows, stream);
+    else
+      e = launch_staged(norm_step_backward_staged<NS, CK, 6>, a, staged_threads(a.d / 4, 6, most), stage, dev,
+                        NORM_BACK_BLOCKS, rows, stream);
+    if (e != cudaSuccess || *rows > 0) return e;
+  }
+  *rows = static_cast<int>(std::min<int64_t>(a.N, 2 * static_cast<int64_t>(dev.sms)));
+  return launch_rows(norm_step_backward_kernel<NS, CK>, a, *rows, stream);
+}
+
 }  // namespace
 
-cudaError_t launch_norm_step(const NormArgs& a, cudaStream_t stream) {
-  const int sms = norm_sms();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int64_t grid = std::min<int64_t>(a.N, static_cast<int64_t>(sms) * 8);
-  return a.n == 1 ? launch_rows(norm_step_kernel<1>, a, grid, stream)
-                  : launch_rows(norm_step_kernel<4>, a, grid, stream);
+cudaError_t launch_norm_step(const NormArgs& args, cudaStream_t stream) {
+  const Device dev = norm_device();
+  NormArgs a = args;
+  a.status = status_word();
+  if (dev.sms <= 0 || a.status == nullptr) return cudaErrorInvalidDevice;
+  return a.n == 1 ? forward_of<1>(a, dev, stream) : forward_of<4>(a, dev, stream);
 }
 
 int norm_backward_rows(int64_t N) {
-  return static_cast<int>(std::min<int64_t>(N, 2 * static_cast<int64_t>(norm_sms())));
+  return static_cast<int>(std::min<int64_t>(N, NORM_BACK_BLOCKS * static_cast<int64_t>(norm_device().sms)));
 }
 
-cudaError_t launch_norm_step_backward(const NormArgs& a, cudaStream_t stream) {
-  const int rows = norm_backward_rows(a.N);
-  if (rows <= 0) return cudaErrorInvalidDevice;
-  cudaError_t e;
-  if (a.X_scale != nullptr)
-    e = a.n == 1 ? launch_rows(norm_step_backward_kernel<1, true>, a, rows, stream)
-                 : launch_rows(norm_step_backward_kernel<4, true>, a, rows, stream);
-  else
-    e = a.n == 1 ? launch_rows(norm_step_backward_kernel<1, false>, a, rows, stream)
-                 : launch_rows(norm_step_backward_kernel<4, false>, a, rows, stream);
+cudaError_t launch_norm_step_backward(const NormArgs& args, cudaStream_t stream) {
+  const Device dev = norm_device();
+  NormArgs a = args;
+  a.status = status_word();
+  if (dev.sms <= 0 || a.status == nullptr) return cudaErrorInvalidDevice;
+  int rows = 0;
+  const bool ck = a.X_scale != nullptr;
+  const cudaError_t e = a.n == 1 ? (ck ? backward_of<1, true>(a, dev, &rows, stream) : backward_of<1, false>(a, dev, &rows, stream))
+                                 : (ck ? backward_of<4, true>(a, dev, &rows, stream) : backward_of<4, false>(a, dev, &rows, stream));
   if (e != cudaSuccess) return e;
   norm_reduce_kernel<<<(norm_partial_floats(a.d) + 31) / 32, 256, 0, stream>>>(a, rows);
   return cudaGetLastError();

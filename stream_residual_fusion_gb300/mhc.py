@@ -10,7 +10,6 @@ lists; outputs are allocated here with torch unless passed in.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -328,28 +327,45 @@ def _need_all(spec):
     for t, dtype, shape, name in spec:
         if t is None:
             continue
+        if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda
+                and t.is_contiguous() and t.get_device() == current):
+            continue
         _need(t, dtype, name)
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.device.index != current:
+        if t.get_device() != current:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{current}")
 
 
-def _on(stream):
-    """Tensors made inside belong to `stream` (the current one if None): the caching allocator hands
-    their memory out again only behind the work queued there."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
-
-
-def _fill(out, shapes, device):
-    """`out` with the missing ones of `shapes` ({name: (shape, dtype)}) allocated, the given ones
-    checked."""
-    o = dict(out or {})
-    _need_all([(o.get(k), dtype, shape, k) for k, (shape, dtype) in shapes.items()])
+def _fill(out, shapes, like, stream):
+    """`out` with the missing ones of `shapes` ({name: (shape, dtype)}) allocated on the device of
+    `like`, the given ones checked. New tensors belong to `stream` (the current one if None): the caching
+    allocator hands their memory out again only behind the work queued there."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _fill(out, shapes, like, None)
+    o = dict(out) if out else {}
+    given = [(o[k], *reversed(shapes[k]), k) for k in shapes if o.get(k) is not None] if o else ()
+    _need_all(given)
     for k, (shape, dtype) in shapes.items():
         if o.get(k) is None:
-            o[k] = torch.empty(shape, dtype=dtype, device=device)
+            o[k] = like.new_empty(shape, dtype=dtype)
     return o
+
+
+def _scratch(nbytes, like, stream):
+    return _fill(None, {"w": ((max(1, nbytes),), torch.uint8)}, like, stream)["w"]
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _queue(stream):
+    """The stream's handle, the current one's if None."""
+    if stream is None:   # torch.cuda.current_stream().cuda_stream without the stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _scale_shape(shape):
@@ -360,13 +376,11 @@ def checkpoint_save(x, out=None, stream=None):
     """mhc_checkpoint_save: bf16 x [..., d] -> (codes uint8 [..., d], scales uint8 [..., ceil(d/32)]),
     the MXFP8 checkpoint of its rows. `out` is a (codes, scales) pair to write to."""
     _need_all([(x, torch.bfloat16, x.shape, "x")])
-    codes, scales = out if out is not None else (None, None)
-    with _on(stream):
-        o = _fill({"codes": codes, "scales": scales},
-                  {"codes": (x.shape, torch.uint8), "scales": (_scale_shape(x.shape), torch.uint8)}, x.device)
+    o = _fill(None if out is None else dict(zip(("codes", "scales"), out)),
+              {"codes": (x.shape, torch.uint8), "scales": (_scale_shape(x.shape), torch.uint8)}, x, stream)
     d = x.shape[-1]
-    _check(lib.mhc_checkpoint_save(_ptr(x), _ptr(o["codes"]), _ptr(o["scales"]), math.prod(x.shape[:-1]), d,
-                                   _stream(stream)), "mhc_checkpoint_save")
+    _check(lib.mhc_checkpoint_save(_at(x), _at(o["codes"]), _at(o["scales"]), math.prod(x.shape[:-1]), d,
+                                   _queue(stream)), "mhc_checkpoint_save")
     return o["codes"], o["scales"]
 
 
@@ -374,10 +388,9 @@ def checkpoint_load(codes, scales, out=None, stream=None):
     """mhc_checkpoint_load: the bf16 rows [..., d] that a checkpoint stands for."""
     _need_all([(codes, torch.uint8, codes.shape, "codes"),
                (scales, torch.uint8, _scale_shape(codes.shape), "scales")])
-    with _on(stream):
-        x = _fill({"x": out}, {"x": (codes.shape, torch.bfloat16)}, codes.device)["x"]
-    _check(lib.mhc_checkpoint_load(_ptr(codes), _ptr(scales), _ptr(x), math.prod(codes.shape[:-1]),
-                                   codes.shape[-1], _stream(stream)), "mhc_checkpoint_load")
+    x = _fill({"x": out}, {"x": (codes.shape, torch.bfloat16)}, codes, stream)["x"]
+    _check(lib.mhc_checkpoint_load(_at(codes), _at(scales), _at(x), math.prod(codes.shape[:-1]),
+                                   codes.shape[-1], _queue(stream)), "mhc_checkpoint_load")
     return x
 
 
@@ -399,20 +412,18 @@ def fused_step_backward_ckpt(X_codes, X_scale, F_codes, F_scale, mixes, pre_prev
                (W, fp, (MIX, n * d), "W"), (scale, fp, (3,), "scale"), (base, fp, (MIX,), "base"),
                (gain, fp, (d,), "gain"), (gXp, bf, (N, n, d), "gXp"), (gy, bf, (N, d), "gy"),
                (gpre, fp, (N, n), "gpre"), (gpost, fp, (N, n), "gpost"), (gcomb, fp, (N, n, n), "gcomb")])
-    with _on(stream):
-        o = _fill(out, {"gX": ((N, n, d), bf), "gF": ((N, d), bf), "gpre_prev": ((N, n), fp),
-                        "gpost_prev": ((N, n), fp), "gcomb_prev": ((N, n, n), fp), "gW": ((MIX, n * d), fp),
-                        "gbase": ((MIX,), fp), "gscale": ((3,), fp), "ggain": ((d,), fp)}, X_codes.device)
-        if workspace is None:
-            workspace = torch.empty(max(1, backward_ckpt_workspace_bytes(N, d, n)), dtype=u8,
-                                    device=X_codes.device)
+    o = _fill(out, {"gX": ((N, n, d), bf), "gF": ((N, d), bf), "gpre_prev": ((N, n), fp),
+                    "gpost_prev": ((N, n), fp), "gcomb_prev": ((N, n, n), fp), "gW": ((MIX, n * d), fp),
+                    "gbase": ((MIX,), fp), "gscale": ((3,), fp), "ggain": ((d,), fp)}, gXp, stream)
+    if workspace is None:
+        workspace = _scratch(backward_ckpt_workspace_bytes(N, d, n), gXp, stream)
     rc = lib.mhc_fused_step_backward_ckpt(
-        _ptr(X_codes), _ptr(X_scale), _ptr(F_codes), _ptr(F_scale), _ptr(mixes), _ptr(pre_prev),
-        _ptr(post_prev), _ptr(comb_prev), _ptr(W), _ptr(scale), _ptr(base), _ptr(gain), _ptr(gXp), _ptr(gy),
-        _ptr(gpre), _ptr(gpost), _ptr(gcomb), _ptr(o["gX"]), _ptr(o["gF"]), _ptr(o["gpre_prev"]),
-        _ptr(o["gpost_prev"]), _ptr(o["gcomb_prev"]), _ptr(o["gW"]), _ptr(o["gbase"]), _ptr(o["gscale"]),
-        _ptr(o["ggain"]), N, n, d, iters, hc_eps, norm_eps, flags, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        _at(X_codes), _at(X_scale), _at(F_codes), _at(F_scale), _at(mixes), _at(pre_prev),
+        _at(post_prev), _at(comb_prev), _at(W), _at(scale), _at(base), _at(gain), _at(gXp), _at(gy),
+        _at(gpre), _at(gpost), _at(gcomb), _at(o["gX"]), _at(o["gF"]), _at(o["gpre_prev"]),
+        _at(o["gpost_prev"]), _at(o["gcomb_prev"]), _at(o["gW"]), _at(o["gbase"]), _at(o["gscale"]),
+        _at(o["ggain"]), N, n, d, iters, hc_eps, norm_eps, flags, _at(workspace),
+        workspace.numel() * workspace.element_size(), _queue(stream))
     _check(rc, "mhc_fused_step_backward_ckpt")
     return o
 
@@ -433,11 +444,10 @@ def norm_step(X, F, gain_post, gain_pre, *, gate=None, pre=None, post=None, comb
     bf = torch.bfloat16
     _need_all([(X, bf, (N, n, d), "X"), (F, bf, (N, d), "F"),
                *_norm_shapes(N, n, d, gain_post, gain_pre, gate, pre, post, comb, flags)])
-    with _on(stream):
-        o = _fill(out, {"Xp": ((N, n, d), bf), "y": ((N, d), bf)}, X.device)
-    rc = lib.mhc_norm_step(_ptr(X), _ptr(F), _ptr(gate), _ptr(pre), _ptr(post), _ptr(comb), _ptr(gain_post),
-                           _ptr(gain_pre), _ptr(o["Xp"]), _ptr(o["y"]), N, n, d, res_scale, norm_eps, flags,
-                           _stream(stream))
+    o = _fill(out, {"Xp": ((N, n, d), bf), "y": ((N, d), bf)}, X, stream)
+    rc = lib.mhc_norm_step(_at(X), _at(F), _at(gate), _at(pre), _at(post), _at(comb), _at(gain_post),
+                           _at(gain_pre), _at(o["Xp"]), _at(o["y"]), N, n, d, res_scale, norm_eps, flags,
+                           _queue(stream))
     _check(rc, "mhc_norm_step")
     return o
 
@@ -459,16 +469,14 @@ def _norm_step_backward(call, where, saved, N, n, d, gXp, gy, gain_post, gain_pr
     if pre is not None:
         rows = () if flags & WEIGHTS_SHARED else (N,)
         shapes.update(gpre=((*rows, n), fp), gpost=((*rows, n), fp), gcomb=((*rows, n, n), fp))
-    with _on(stream):
-        o = _fill(out, shapes, gXp.device)
-        if workspace is None:
-            workspace = torch.empty(max(1, norm_step_backward_workspace_bytes(N, d, n)), dtype=torch.uint8,
-                                    device=gXp.device)
-    rc = call(*[_ptr(t) for t, _, _, _ in saved], _ptr(gate), _ptr(pre), _ptr(post), _ptr(comb),
-              _ptr(gain_post), _ptr(gain_pre), _ptr(gXp), _ptr(gy), _ptr(o["gX"]), _ptr(o["gF"]),
-              _ptr(o.get("ggate")), _ptr(o.get("gpre")), _ptr(o.get("gpost")), _ptr(o.get("gcomb")),
-              _ptr(o.get("ggain_post")), _ptr(o["ggain_pre"]), N, n, d, res_scale, norm_eps, flags,
-              _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    o = _fill(out, shapes, gXp, stream)
+    if workspace is None:
+        workspace = _scratch(norm_step_backward_workspace_bytes(N, d, n), gXp, stream)
+    rc = call(*[_at(t) for t, _, _, _ in saved], _at(gate), _at(pre), _at(post), _at(comb),
+              _at(gain_post), _at(gain_pre), _at(gXp), _at(gy), _at(o["gX"]), _at(o["gF"]),
+              _at(o.get("ggate")), _at(o.get("gpre")), _at(o.get("gpost")), _at(o.get("gcomb")),
+              _at(o.get("ggain_post")), _at(o["ggain_pre"]), N, n, d, res_scale, norm_eps, flags,
+              _at(workspace), workspace.numel() * workspace.element_size(), _queue(stream))
     _check(rc, where)
     return o
 
