@@ -38,17 +38,14 @@
 #include <algorithm>
 #include <mutex>
 
+#include "bwd_parts.cuh"
 #include "hc_arith.cuh"
 #include "internal.h"
 #include "layout.cuh"
-#include "mx8.cuh"
 #include "ptx.cuh"
 
 namespace mhc {
 namespace {
-
-constexpr int MIXN = 24;
-constexpr uint64_t BWD_WAIT_NS = 2000000000ull;   // 2 s
 
 // ---------------------------------------------------------------------------------------------
 // bwd_mix_kernel
@@ -56,13 +53,6 @@ constexpr uint64_t BWD_WAIT_NS = 2000000000ull;   // 2 s
 constexpr int MIX_THREADS = 64;
 constexpr int CK_EVERY = 8;         // least Sinkhorn checkpoint spacing (steps)
 constexpr int CK_MAX = 6;           // checkpoints held per token (shared memory)
-
-// Reciprocal of a positive normal float within 1 ulp (the hardware approximation).
-__device__ __forceinline__ float rcp_fast(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // One Sinkhorn normalisation of c in place: step i even divides columns, odd divides rows.
 __device__ __forceinline__ void sk_step(float (&c)[16], int i, float eps) {
@@ -109,8 +99,6 @@ __device__ __forceinline__ void sk_step_back(float (&g)[16], const float (&c)[16
     }
   }
 }
-
-__device__ __forceinline__ float sigmoid_b(float z) { return 1.0f / (1.0f + expf(-z)); }
 
 __global__ void __launch_bounds__(MIX_THREADS) bwd_mix_kernel(
     const float* __restrict__ mixes, const float* __restrict__ gpre, const float* __restrict__ gpost,
@@ -805,15 +793,6 @@ constexpr int WT_CONS = 4;                   // consumer / epilogue warps (2..5)
 constexpr int WT_THREADS = (2 + WT_CONS) * 32;
 constexpr uint32_t WT_TMEM_COLS = 128;
 
-// Shared-memory descriptor of an MN-major operand: `row_bytes` (64 or 128) of the MN dimension
-// per row with the swizzle of that width, consecutive K rows row_bytes apart, 8-row K groups
-// `sbo` bytes apart, the next MN atom `lbo` bytes on.
-__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t saddr, int row_bytes, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(row_bytes == 128 ? 2 : 4) << 61);
-}
-
 struct WtParams {
   float* partW;
   float* partG;
@@ -1057,102 +1036,7 @@ __global__ void __launch_bounds__(256) bwd_reduce_kernel(
 }
 
 // ---------------------------------------------------------------------------------------------
-// Checkpoints of X and F to bf16 X, F and X' = hc_post(X, F): one thread per 8 columns of a token.
-__global__ void expand_kernel(const uint2* __restrict__ Xc, const uint8_t* __restrict__ Xs,
-                              const uint2* __restrict__ Fc, const uint8_t* __restrict__ Fs,
-                              const float* __restrict__ post, const float* __restrict__ comb,
-                              uint4* __restrict__ X, uint4* __restrict__ F, uint4* __restrict__ Xp,
-                              int64_t N, int d, int row_dest, float neg_zero) {
-  const int chunks = d / 8, blocks = d / MX_BLOCK;
-  const int64_t total = N * chunks;
-  for (int64_t idx = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; idx < total;
-       idx += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t t = idx / chunks;
-    const int c = static_cast<int>(idx - t * chunks);
-    auto rows = [&](const uint2* codes, const uint8_t* scales, int64_t row, f2 (&v)[4]) {
-      const uint2 w = __ldg(codes + row * chunks + c);
-      const float sv = scale_value(__ldg(scales + row * blocks + c / 4));
-      const f2 s{sv, sv};
-      v[0] = decode2(w.x, s);
-      v[1] = decode2(w.x >> 16, s);
-      v[2] = decode2(w.y, s);
-      v[3] = decode2(w.y >> 16, s);
-    };
-    f2 x[4][4], f[4];
-    rows(Fc, Fs, t, f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) rows(Xc, Xs, t * 4 + j, x[j]);
-    uint32_t o[4][4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float uk = __ldg(post + t * 4 + k);
-      f2 ck[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v = __ldg(comb + t * 16 + (row_dest ? k * 4 + j : j * 4 + k));
-        ck[j] = f2{v, v};
-      }
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const f2 xw[4] = {x[0][w], x[1][w], x[2][w], x[3][w]};
-        o[k][w] = f2_to_bf2(hc_post_pair(ck, f2{uk, uk}, xw, f[w], f2{neg_zero, neg_zero}));
-      }
-    }
-    F[idx] = make_uint4(f2_to_bf2(f[0]), f2_to_bf2(f[1]), f2_to_bf2(f[2]), f2_to_bf2(f[3]));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t at = (t * 4 + k) * chunks + c;
-      X[at] = make_uint4(f2_to_bf2(x[k][0]), f2_to_bf2(x[k][1]), f2_to_bf2(x[k][2]), f2_to_bf2(x[k][3]));
-      Xp[at] = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------------------------
 // host side
-
-// No L2 promotion: a CTA of these kernels reads the neighbouring columns of a row only slots
-// later, so fetching them early only adds traffic.
-bool bmap(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-          const cuuint32_t* box, CUtensorMapSwizzle swz) {
-  auto fn = tensor_map_encoder();
-  if (fn == nullptr) return false;
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-bool bmap_streams(CUtensorMap* m, const void* p, int64_t N, int d, uint32_t rows) {   // [N, 4, d]
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), 4, static_cast<cuuint64_t>(N)};
-  const cuuint64_t str[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(d) * 8};
-  const cuuint32_t box[3] = {BDC, 1, rows};
-  return bmap(m, p, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B);
-}
-bool bmap_streams_box(CUtensorMap* m, const void* p, int64_t N, int d, uint32_t cols, uint32_t rows,
-                      CUtensorMapSwizzle swz) {   // [N, 4, d], boxes of [rows x cols] of one stream
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), 4, static_cast<cuuint64_t>(N)};
-  const cuuint64_t str[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(d) * 8};
-  const cuuint32_t box[3] = {cols, 1, rows};
-  return bmap(m, p, 3, dims, str, box, swz);
-}
-bool bmap_rows(CUtensorMap* m, const void* p, int64_t N, int cols, uint32_t box_cols, uint32_t rows,
-               CUtensorMapSwizzle swz) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(N)};
-  const cuuint64_t str[1] = {static_cast<cuuint64_t>(cols) * 2};
-  const cuuint32_t box[2] = {box_cols, rows};
-  return bmap(m, p, 2, dims, str, box, swz);
-}
-
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
-int gcd_i(int a, int b) { return b == 0 ? a : gcd_i(b, a % b); }
-
-size_t a256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -1290,34 +1174,6 @@ cudaError_t launch_backward(const BwdArgs& a, cudaStream_t stream) {
                                                   a.ggain, a.gbase, a.gscale, d, L.ranges, L.blocks0);
   }
   return cudaGetLastError();
-}
-
-size_t bwd_ckpt_bytes(int64_t N, int d) {
-  const size_t base = bwd_layout(N, d).bytes;
-  if (base == 0) return 0;
-  const size_t streams = a256(static_cast<size_t>(N) * 8 * d), rows = a256(static_cast<size_t>(N) * 2 * d);
-  return a256(base) + 2 * streams + rows;
-}
-
-cudaError_t launch_backward_ckpt(const BwdArgs& args, const BwdCheckpoint& c, cudaStream_t stream) {
-  BwdArgs a = args;
-  const size_t base = a256(bwd_layout(a.N, a.d).bytes);
-  const size_t streams = a256(static_cast<size_t>(a.N) * 8 * a.d);
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  uint4* X = reinterpret_cast<uint4*>(ws + base);
-  uint4* Xp = reinterpret_cast<uint4*>(ws + base + streams);
-  uint4* F = reinterpret_cast<uint4*>(ws + base + 2 * streams);
-  const int64_t work = a.N * (a.d / 8);
-  expand_kernel<<<static_cast<int>(std::min<int64_t>((work + 255) / 256, 16 * sm_count())), 256, 0, stream>>>(
-      static_cast<const uint2*>(c.X_codes), static_cast<const uint8_t*>(c.X_scale),
-      static_cast<const uint2*>(c.F_codes), static_cast<const uint8_t*>(c.F_scale), a.post_prev, a.comb_prev, X,
-      F, Xp, a.N, a.d, static_cast<int>(a.flags & 1u), -0.0f);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  a.X = X;
-  a.F = F;
-  a.Xp = Xp;
-  return launch_backward(a, stream);
 }
 
 }  // namespace mhc

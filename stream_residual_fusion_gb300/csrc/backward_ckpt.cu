@@ -1,0 +1,1121 @@
+// backward_ckpt.cu -- gradients of the single-pass mHC step from 8-bit checkpoints of its inputs.
+//
+// The formulas are those of backward.cu at X^, F^ (the decoded checkpoints), X' = bf16(hc_post(X^, F^)),
+// y_hat = bf16(hc_pre(X')) and the forward's mix numbers m. A pass over a token reads 5.16 d bytes of
+// codes and scales where backward.cu reads 8 d of X' or 10 d of X and F.
+//
+// Four launches on the caller's stream:
+//   ckb_prep_kernel    the split's and Sinkhorn's derivatives (g_m), four lanes a token, one row of the
+//                      4 x 4 matrix each; beside them, in blocks of their own, the bf16 planes of W^T.
+//   ckb_token_kernel   one block a token: the sums over its width that give r, r_y, tau, c1 and gp, the
+//                      three bf16 planes of r g_m, and ggain, which gathers in the threads' registers.
+//   ckb_stream_kernel  work items of (64 columns of every stream, a range of token tiles): gX, gF, and
+//                      gW, for which X' never leaves the SM (below).
+//   ckb_reduce_kernel  sums of partials in a fixed order: gW, ggain, g_base, g_scale, and gu, gC of every
+//                      token over the column blocks.
+//
+// Why the stream kernel owns columns and walks tokens: W^T of its columns stays in shared memory, the
+// gW accumulators stay in TMEM over the range, X' feeds its tensor-core product from shared memory
+// right after it was formed (backward.cu reads X' and gy a second time for that), and a few tokens
+// already give every SM work: d / 64 items a tile. The price is gu and gC in d / 64 parts, 1.25 d bytes a
+// token written and read again.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "block_sums.cuh"
+#include "bwd_parts.cuh"
+#include "hc_arith.cuh"
+#include "internal.h"
+#include "layout.cuh"
+#include "mx8.cuh"
+#include "ptx.cuh"
+
+namespace mhc {
+namespace {
+
+// hi + mid + lo = v to 2^-26 of v: three bf16 planes, each the rounding of what the others left
+struct Planes {
+  __nv_bfloat16 p[3];
+};
+__device__ __forceinline__ Planes planes_of(float v) {
+  Planes o;
+  o.p[0] = __float2bfloat16_rn(v);
+  const float rest = v - __bfloat162float(o.p[0]);
+  o.p[1] = __float2bfloat16_rn(rest);
+  o.p[2] = __float2bfloat16_rn(rest - __bfloat162float(o.p[1]));
+  return o;
+}
+
+// ---------------------------------------------------------------------------------------------
+// ckb_prep_kernel
+
+constexpr int PREP_THREADS = 128;
+constexpr int PREP_TOKENS = PREP_THREADS / 4;
+// Sinkhorn step inputs kept a token (shared memory, 64 bytes each): all of them up to 24 rounds, every
+// second one up to 48, ...
+constexpr int PREP_KEEP = 47;
+constexpr int SB_COLS = 64;                      // columns of a work item of the stream kernel
+constexpr int W_HM = 128 * 128;                  // W^T hi and mid planes of 32 columns: 128 rows x 128 bytes
+constexpr int W_LO = 128 * 64;                   // lo plane
+constexpr int W_SLOT = W_HM + W_LO;
+
+// Sum over the four lanes of a token.
+__device__ __forceinline__ float sum4(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+// Normalisation i of this lane's row: even steps divide columns, odd ones rows.
+__device__ __forceinline__ void row_step(float (&c)[4], int i, float eps) {
+  if ((i & 1) == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] *= rcp_fast(sum4(c[k]) + eps);
+  } else {
+    const float r = rcp_fast(((c[0] + c[1]) + (c[2] + c[3])) + eps);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] *= r;
+  }
+}
+__device__ __forceinline__ void row_step_back(float (&g)[4], const float (&c)[4], int i, float eps) {
+  if ((i & 1) == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float inv = rcp_fast(sum4(c[k]) + eps);
+      g[k] = g[k] * inv - sum4(g[k] * c[k]) * inv * inv;
+    }
+  } else {
+    const float inv = rcp_fast(((c[0] + c[1]) + (c[2] + c[3])) + eps);
+    const float t = ((g[0] * c[0] + g[1] * c[1]) + (g[2] * c[2] + g[3] * c[3])) * inv * inv;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) g[k] = g[k] * inv - t;
+  }
+}
+
+// W^T planes of slot s (columns 32 s .. 32 s + 31 of every stream): row 32 k + c for column c of stream
+// k, 64 bf16 (hi[0..23], 8 zeros, mid[0..23], 8 zeros) with the 128-byte swizzle, then 32 bf16
+// (lo[0..23], 8 zeros) a row with the 64-byte swizzle. One row a thread.
+__device__ void pack_rows(const float* __restrict__ W, uint8_t* __restrict__ out, int d, int64_t idx) {
+  const int64_t K = 4 * static_cast<int64_t>(d);
+  const int row = static_cast<int>(idx % 128);
+  const int64_t s = idx / 128;
+  const int64_t col = (row / 32) * static_cast<int64_t>(d) + s * 32 + row % 32;
+  uint32_t w[3][16];
+#pragma unroll
+  for (int o = 0; o < 16; ++o) {
+    Planes a = planes_of(0.f), b = a;
+    if (2 * o < MIXN) {
+      a = planes_of(__ldg(W + (2 * o) * K + col));
+      b = planes_of(__ldg(W + (2 * o + 1) * K + col));
+    }
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl)
+      w[pl][o] = static_cast<uint32_t>(__bfloat16_as_ushort(a.p[pl])) |
+                 (static_cast<uint32_t>(__bfloat16_as_ushort(b.p[pl])) << 16);
+  }
+  uint8_t* base = out + s * W_SLOT;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    auto put = [&](uint8_t* p, const uint32_t (&v)[16]) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    };
+    put(base + swizzled_chunk_offset(row, c, 128), w[0]);
+    put(base + swizzled_chunk_offset(row, 4 + c, 128), w[1]);
+    put(base + W_HM + swizzled_chunk_offset(row, c, 64), w[2]);
+  }
+}
+
+__global__ void __launch_bounds__(PREP_THREADS) ckb_prep_kernel(
+    const float* __restrict__ mixes, const float* __restrict__ gpre, const float* __restrict__ gpost,
+    const float* __restrict__ gcomb, const float* __restrict__ scale, const float* __restrict__ base,
+    const float* __restrict__ W, float* __restrict__ gm, float* __restrict__ part, uint8_t* __restrict__ wT,
+    int64_t N, int d, int iters, float eps, int mix_blocks, int every) {
+  extern __shared__ float4 kept[];   // [step / every][thread]
+  __shared__ float red[PREP_THREADS / 32][MIXN + 3];
+  if (static_cast<int>(blockIdx.x) >= mix_blocks) {
+    const int64_t idx = (blockIdx.x - mix_blocks) * static_cast<int64_t>(PREP_THREADS) + threadIdx.x;
+    if (idx < static_cast<int64_t>(d / 32) * 128) pack_rows(W, wT, d, idx);
+    return;
+  }
+  const int64_t t = blockIdx.x * static_cast<int64_t>(PREP_TOKENS) + threadIdx.x / 4;
+  const int j = threadIdx.x & 3;
+  const bool in = t < N;
+  auto at = [&](const float* p, int64_t i) { return in ? __ldg(p + i) : 0.f; };
+  auto at4 = [&](const float* p, int64_t i, float (&v)[4]) {
+    const float4 q = in ? __ldg(reinterpret_cast<const float4*>(p + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+  };
+  const float s0 = __ldg(scale), s1 = __ldg(scale + 1), s2 = __ldg(scale + 2);
+  const float mp = at(mixes, t * MIXN + j), mu = at(mixes, t * MIXN + 4 + j);
+  float ml[4], sm[4], c[4], g[4], b[4];
+  at4(mixes, t * MIXN + 8 + 4 * j, ml);
+  at4(gcomb, t * 16 + 4 * j, g);
+  // p_j = sigmoid(s0 m_j + b_j) + eps, u_j = 2 sigmoid(s1 m_4+j + b_4+j)
+  const float sp = sigmoid_b(fmaf(s0, mp, __ldg(base + j))), su = sigmoid_b(fmaf(s1, mu, __ldg(base + 4 + j)));
+  const float gzp = at(gpre, t * 4 + j) * sp * (1.0f - sp), gzu = 2.0f * at(gpost, t * 4 + j) * su * (1.0f - su);
+  // softmax of row j of the logits, then + eps
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sm[k] = fmaf(s2, ml[k], __ldg(base + 8 + 4 * j + k));
+  const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sm[k] = expf(sm[k] - mx);
+  const float inv = 1.0f / ((sm[0] + sm[1]) + (sm[2] + sm[3]));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    sm[k] *= inv;
+    c[k] = sm[k] + eps;
+  }
+  // the steps, their inputs kept every `every` steps; then each step's derivative at its input
+  const int steps = 2 * iters - 1;
+  for (int i = 0; i < steps; ++i) {
+    if (i % every == 0) kept[(i / every) * PREP_THREADS + threadIdx.x] = make_float4(c[0], c[1], c[2], c[3]);
+    row_step(c, i, eps);
+  }
+  for (int i = steps - 1; i >= 0; --i) {
+    const float4 q = kept[(i / every) * PREP_THREADS + threadIdx.x];
+    c[0] = q.x; c[1] = q.y; c[2] = q.z; c[3] = q.w;
+    for (int n = i / every * every; n < i; ++n) row_step(c, n, eps);
+    row_step_back(g, c, i, eps);
+  }
+  const float dot = (g[0] * sm[0] + g[1] * sm[1]) + (g[2] * sm[2] + g[3] * sm[3]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) b[k] = sm[k] * (g[k] - dot);   // gradient of the logits
+  if (in) {
+    gm[t * MIXN + j] = s0 * gzp;
+    gm[t * MIXN + 4 + j] = s1 * gzu;
+    *reinterpret_cast<float4*>(gm + t * MIXN + 8 + 4 * j) = make_float4(s2 * b[0], s2 * b[1], s2 * b[2], s2 * b[3]);
+  }
+  // the block's sums of g_base (0..23) and g_scale (24..26)
+  float v[9] = {gzp, gzu, b[0], b[1], b[2], b[3], gzp * mp, gzu * mu,
+                (b[0] * ml[0] + b[1] * ml[1]) + (b[2] * ml[2] + b[3] * ml[3])};
+#pragma unroll
+  for (int i = 0; i < 9; ++i) {
+#pragma unroll
+    for (int o = 16; o >= 4; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (i >= 6) v[i] = sum4(v[i]);
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane < 4) {
+    red[warp][j] = v[0];
+    red[warp][4 + j] = v[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) red[warp][8 + 4 * j + k] = v[2 + k];
+    if (lane < 3) red[warp][MIXN + lane] = lane == 0 ? v[6] : lane == 1 ? v[7] : v[8];
+  }
+  __syncthreads();
+  if (threadIdx.x < MIXN + 3) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < PREP_THREADS / 32; ++w) s += red[w][threadIdx.x];
+    part[static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// ckb_token_kernel
+
+constexpr int TOKEN_WARPS = 12;     // warps of a block, at most
+
+struct CkIn {
+  const uint2* X;          // codes [N, 4, d], 8 to a word pair
+  const uint8_t* Xs;       // scales [N, 4, d / 32]
+  const uint2* F;
+  const uint8_t* Fs;
+};
+
+template <int CH>
+__global__ void __launch_bounds__(TOKEN_WARPS * 32) ckb_token_kernel(
+    const CkIn in, const uint4* __restrict__ gy, const float* __restrict__ pre, const float* __restrict__ post,
+    const float* __restrict__ comb, const float* __restrict__ gain, const float* __restrict__ mixes,
+    const float* __restrict__ gm, float* __restrict__ rec, __nv_bfloat16* __restrict__ planes_hm,
+    __nv_bfloat16* __restrict__ planes_lo, float* __restrict__ gpre_prev, float* __restrict__ part_gain,
+    int64_t N, int d, float norm_eps, int row_dest, float neg_zero) {
+  // |x|^2, |y_hat|^2, T, gain gy . X'_j, y_hat . X'_j
+  constexpr int V = 16;
+  __shared__ float scratch[2][TOKEN_WARPS * V];
+  const int T = blockDim.x, warps = T / 32, lane = threadIdx.x & 31;
+  const int chunks = d / 8, blocks = d / MX_BLOCK;
+  const f2 nz{neg_zero, neg_zero};
+  const float fd = static_cast<float>(d), fk = 4.0f * fd;
+  f2 sum_gain[CH][4];
+#pragma unroll
+  for (int q = 0; q < CH; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum_gain[q][i] = f2{0.f, 0.f};
+  int n = 0;
+  for (int64_t t = blockIdx.x; t < N; t += gridDim.x, ++n) {
+    uint2 xc[CH][4], fc[CH];
+    uint32_t xs[CH], fs[CH];
+    uint4 gyw[CH];
+#pragma unroll
+    for (int q = 0; q < CH; ++q) {
+      const int c = static_cast<int>(threadIdx.x) + q * T;
+      if (c >= chunks) break;
+      xs[q] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        xc[q][k] = __ldg(in.X + (t * 4 + k) * chunks + c);
+        xs[q] |= static_cast<uint32_t>(__ldg(in.Xs + (t * 4 + k) * blocks + c / 4)) << (8 * k);
+      }
+      fc[q] = __ldg(in.F + t * chunks + c);
+      fs[q] = __ldg(in.Fs + t * blocks + c / 4);
+      gyw[q] = __ldg(gy + t * chunks + c);
+    }
+    float gmi = 0.f, mi = 0.f;
+    if (threadIdx.x < MIXN) {
+      gmi = __ldg(gm + t * MIXN + threadIdx.x);
+      mi = __ldg(mixes + t * MIXN + threadIdx.x);
+    }
+    f2 cc[4][4], cu[4], cp[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float u = __ldg(post + t * 4 + k), p = __ldg(pre + t * 4 + k);
+      cu[k] = f2{u, u};
+      cp[k] = f2{p, p};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float w = __ldg(comb + t * 16 + (row_dest ? 4 * k + j : 4 * j + k));
+        cc[j][k] = f2{w, w};
+      }
+    }
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.f;
+    auto dot = [&](int i, f2 a, f2 b) { v[i] = fmaf(a.x, b.x, fmaf(a.y, b.y, v[i])); };
+    f2 gyy[CH][4];   // gy y_hat, for ggain
+#pragma unroll
+    for (int q = 0; q < CH; ++q) {
+      const int c = static_cast<int>(threadIdx.x) + q * T;
+      if (c >= chunks) break;
+      const float4 g0 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * c);
+      const float4 g1 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * c + 1);
+      const f2 ga[4] = {f2{g0.x, g0.y}, f2{g0.z, g0.w}, f2{g1.x, g1.y}, f2{g1.z, g1.w}};
+      const uint32_t gw[4] = {gyw[q].x, gyw[q].y, gyw[q].z, gyw[q].w};
+      f2 sx[4], sf;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float s = scale_value((xs[q] >> (8 * k)) & 0xffu);
+        sx[k] = f2{s, s};
+      }
+      const float s = scale_value(fs[q]);
+      sf = f2{s, s};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        auto word = [&](uint2 w) { return (i < 2 ? w.x : w.y) >> (16 * (i & 1)); };
+        f2 x[4], xp[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = decode2(word(xc[q][k]), sx[k]);
+        const f2 f = decode2(word(fc[q]), sf);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const f2 ck[4] = {cc[0][k], cc[1][k], cc[2][k], cc[3][k]};
+          xp[k] = bf2_to_f2(f2_to_bf2(hc_post_pair(ck, cu[k], x, f, nz)));
+          dot(0, xp[k], xp[k]);
+        }
+        const f2 yh = bf2_to_f2(f2_to_bf2(hc_pre_pair(cp, xp, nz)));
+        const f2 g = bf2_to_f2(gw[i]);
+        const f2 gg = mul2(ga[i], g);
+        dot(1, yh, yh);
+        dot(2, gg, yh);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          dot(3 + k, gg, xp[k]);
+          dot(7 + k, yh, xp[k]);
+        }
+        gyy[q][i] = mul2(g, yh);
+      }
+    }
+    const float tot = group_sums<V>(v, scratch[n & 1], warps, T);
+    const float ry = __frsqrt_rn(__fdiv_rn(lane_value(tot, 1), fd) + norm_eps);
+#pragma unroll
+    for (int q = 0; q < CH; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (static_cast<int>(threadIdx.x) + q * T < chunks) sum_gain[q][i] = fma2(f2{ry, ry}, gyy[q][i], sum_gain[q][i]);
+    if (threadIdx.x < 32) {
+      const float r = __frsqrt_rn(__fdiv_rn(lane_value(tot, 0), fk) + norm_eps);
+      const float tau = ry * ry * ry * lane_value(tot, 2) / fd;
+      float gmm = gmi * mi;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) gmm += __shfl_xor_sync(0xffffffffu, gmm, o);
+      const float c1 = r * r / fk * gmm;
+      const Planes p = planes_of(r * gmi);   // lanes 24..31: zero columns
+      planes_hm[t * 64 + lane] = p.p[0];
+      planes_hm[t * 64 + 32 + lane] = p.p[1];
+      planes_lo[t * 32 + lane] = p.p[2];
+      const float gp = ry * tot - tau * __shfl_down_sync(0xffffffffu, tot, 4);
+      if (lane >= 3 && lane < 7) gpre_prev[t * 4 + lane - 3] = gp;
+      if (lane == 0) reinterpret_cast<float4*>(rec)[t] = make_float4(r, ry, tau, c1);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < CH; ++q) {
+    const int c = static_cast<int>(threadIdx.x) + q * T;
+    if (c >= chunks) break;
+    float4* o = reinterpret_cast<float4*>(part_gain + blockIdx.x * static_cast<int64_t>(d)) + 2 * c;
+    o[0] = make_float4(sum_gain[q][0].x, sum_gain[q][0].y, sum_gain[q][1].x, sum_gain[q][1].y);
+    o[1] = make_float4(sum_gain[q][2].x, sum_gain[q][2].y, sum_gain[q][3].x, sum_gain[q][3].y);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// ckb_stream_kernel: per work item, W^T (r g_m) and gW on the tensor cores around the elementwise
+// gradients. A tile is up to 112 tokens; a slot is 32 columns of every stream of a tile.
+//   warp 0, lane 0   TMA loads: codes (2 slots ahead), gXp and gy (2 slots), the tile's planes of r g_m.
+//   warp 0, lane 1   TMA stores of gX, gF, which were written over gXp and gy.
+//   warp 1, lane 0   W^T of the item's columns, and the MMAs: D = A W^T^T for the next slot (A = the planes
+//                    [tokens x 24] of r g_m, six products of planes, the three largest orders), then
+//                    gW += X'^T A of this slot once the consumers have laid X' down.
+//   warps 2..9       two threads a token, 16 columns of the slot each.
+
+constexpr int SBT = 128;                     // rows of D
+constexpr int SBR = 112;                     // token rows of a tile, at most
+constexpr int SB_CODE = SBR * 32;            // codes of one stream (or F): [112 x 32] bytes
+constexpr int SB_CODES = 5 * SB_CODE;
+constexpr int SB_TILE = SBR * 64;            // [112 x 32] bf16
+constexpr int SB_SET = 5 * SB_TILE;
+constexpr int SB_PHM = SBR * 128;            // planes of r g_m: hi and mid
+constexpr int SB_PLO = SBR * 64;
+constexpr int SO_PHM = 0;                    // two of each, then the item's W^T (two slots)
+constexpr int SO_WHM = SO_PHM + 2 * SB_PHM;
+constexpr int SO_WLO = SO_WHM + 2 * W_HM;
+constexpr int SO_PLO = SO_WLO + 2 * W_LO;
+constexpr int SO_XP = SO_PLO + 2 * SB_PLO;   // X' of the slot, [112 x 32] bf16 of each stream
+constexpr int SO_B = SO_XP + 4 * SB_TILE;    // gXp, gy -> gX, gF
+constexpr int SO_C = SO_B + 2 * SB_SET;      // codes
+constexpr int SO_BARS = SO_C + 2 * SB_CODES;
+constexpr int SB_NBARS = 2 * 9 + 6;
+constexpr int SO_TMEM = SO_BARS + SB_NBARS * 8;
+constexpr int SB_SMEM = SO_TMEM + 16 + 1024;
+static_assert(SB_SMEM <= 232448, "shared memory budget");
+static_assert(SB_PHM % 1024 == 0 && W_HM % 1024 == 0 && SO_PLO % 1024 == 0 && SB_PLO % 512 == 0 &&
+                  SB_TILE % 512 == 0 && SB_CODE % 256 == 0 && SO_XP % 512 == 0 && SO_C % 256 == 0,
+              "tile alignment");
+// D reads 128 rows of an A tile of at most 112: what lies behind it is other data of this block
+static_assert(SO_PLO + SB_PLO + 128 * 64 <= SO_BARS, "operand rows");
+constexpr int SB_CONS = 8;
+constexpr int SB_THREADS = (2 + SB_CONS) * 32;
+constexpr uint32_t SB_TMEM = 512;            // D twice 128 columns, gW twice 96 from column 256
+
+struct SbParams {
+  const float* pre;
+  const float* post;
+  const float* comb;
+  const float* rec;
+  const float* gain;
+  const uint8_t* Xs;
+  const uint8_t* Fs;
+  const uint8_t* wT;
+  float* part_w;       // [ranges][24][4 d]
+  float* part_t;       // [d / 64][N][20]: gu, gC (as gcomb_prev is laid out)
+  unsigned* status;
+  int N;
+  int d;
+  int tt;              // token rows of a tile, a multiple of 16
+  int ntiles;
+  int per;             // tiles of a range
+  int ranges;
+  float neg_zero;
+  int row_dest;
+};
+
+__global__ void __launch_bounds__(SB_THREADS, 1)
+    ckb_stream_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_f,
+                      const __grid_constant__ CUtensorMap tm_gxp, const __grid_constant__ CUtensorMap tm_gy,
+                      const __grid_constant__ CUtensorMap tm_gx, const __grid_constant__ CUtensorMap tm_gf,
+                      const __grid_constant__ CUtensorMap tm_hm, const __grid_constant__ CUtensorMap tm_lo,
+                      const SbParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  uint64_t* cfull = reinterpret_cast<uint64_t*>(sm + SO_BARS);
+  uint64_t* cempty = cfull + 2;
+  uint64_t* bfull = cempty + 2;
+  uint64_t* bempty = bfull + 2;
+  uint64_t* gready = bempty + 2;
+  uint64_t* dready = gready + 2;
+  uint64_t* dfree = dready + 2;
+  uint64_t* pfull = dfree + 2;
+  uint64_t* pempty = pfull + 2;
+  uint64_t* wfull = pempty + 2;
+  uint64_t* wempty = wfull + 1;
+  uint64_t* xready = wempty + 1;
+  uint64_t* xfree = xready + 1;
+  uint64_t* gwfull = xfree + 1;
+  uint64_t* gwfree = gwfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SO_TMEM);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tt = P.tt;
+  const int nblocks = P.d / SB_COLS;
+  const int items = nblocks * P.ranges;
+  bool timed_out = false;
+  auto limit = [&]() { return timed_out ? 0ull : BWD_WAIT_NS; };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!mbar_wait(bar, parity & 1, limit())) timed_out = true;
+  };
+  // the tiles of an item
+  auto first_tile = [&](int item) { return item / nblocks * P.per; };
+  auto last_tile = [&](int item) { return min(P.ntiles, first_tile(item) + P.per); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&cfull[i], 1);
+      mbar_init(&cempty[i], SB_CONS);
+      mbar_init(&bfull[i], 1);
+      mbar_init(&bempty[i], 1);
+      mbar_init(&gready[i], SB_CONS);
+      mbar_init(&dready[i], 1);
+      mbar_init(&dfree[i], SB_CONS);
+      mbar_init(&pfull[i], 1);
+      mbar_init(&pempty[i], 1);
+    }
+    mbar_init(wfull, 1);
+    mbar_init(wempty, 1);
+    mbar_init(xready, SB_CONS);
+    mbar_init(xfree, 1);
+    mbar_init(gwfull, 1);
+    mbar_init(gwfree, SB_CONS);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, SB_TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  block_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- loads
+      const uint64_t pol = policy_evict_first();
+      const uint32_t code_bytes = 5u * 32u * tt, b_bytes = 5u * 64u * tt;
+      int u = 0, tn = 0;   // slots and tiles of this block so far
+      for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int cb = item % nblocks;
+        for (int tile = first_tile(item); tile < last_tile(item); ++tile, ++tn) {
+          const int t0 = tile * tt, pb = tn & 1;
+          if (tn >= 2) wait(&pempty[pb], (tn >> 1) - 1);
+          mbar_arrive_expect_tx(&pfull[pb], static_cast<uint32_t>(192 * tt));
+          tma_load_2d(sm + SO_PHM + pb * SB_PHM, &tm_hm, &pfull[pb], 0, t0);
+          tma_load_2d(sm + SO_PLO + pb * SB_PLO, &tm_lo, &pfull[pb], 0, t0);
+          for (int s = 0; s < 2; ++s, ++u) {
+            const int e = u & 1, col = cb * SB_COLS + 32 * s;
+            if (u >= 2) wait(&cempty[e], (u >> 1) - 1);
+            mbar_arrive_expect_tx(&cfull[e], code_bytes);
+            uint8_t* c = sm + SO_C + e * SB_CODES;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tma_load_3d_hint(c + k * SB_CODE, &tm_x, &cfull[e], col, k, t0, pol);
+            tma_load_2d_hint(c + 4 * SB_CODE, &tm_f, &cfull[e], col, t0, pol);
+            if (u >= 2) wait(&bempty[e], (u >> 1) - 1);
+            mbar_arrive_expect_tx(&bfull[e], b_bytes);
+            uint8_t* b = sm + SO_B + e * SB_SET;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tma_load_3d_hint(b + k * SB_TILE, &tm_gxp, &bfull[e], col, k, t0, pol);
+            tma_load_2d_hint(b + 4 * SB_TILE, &tm_gy, &bfull[e], col, t0, pol);
+          }
+        }
+      }
+    } else if (lane == 1) {
+      // ---------------------------------------------------------------- stores
+      const uint64_t pol = policy_evict_first();
+      int u = 0;
+      for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int cb = item % nblocks;
+        for (int tile = first_tile(item); tile < last_tile(item); ++tile) {
+          for (int s = 0; s < 2; ++s, ++u) {
+            const int e = u & 1, col = cb * SB_COLS + 32 * s, t0 = tile * tt;
+            wait(&gready[e], u >> 1);
+            const uint8_t* b = sm + SO_B + e * SB_SET;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tma_store_3d_hint(&tm_gx, b + k * SB_TILE, col, k, t0, pol);
+            tma_store_2d_hint(&tm_gf, b + 4 * SB_TILE, col, t0, pol);
+            bulk_commit();
+            bulk_wait_read<0>();
+            mbar_arrive(&bempty[e]);
+          }
+        }
+      }
+      bulk_wait<0>();
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------------------------------------------------------- MMAs
+      constexpr uint32_t id_d = idesc_bf16_f32(128, 128);
+      constexpr uint32_t id_hm = idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16);   // both MN-major
+      constexpr uint32_t id_lo = idesc_bf16_f32(128, 32) | (1u << 15) | (1u << 16);
+      const uint64_t wpol = policy_evict_last();
+      // where the product of slot u (u the slot's number in this block) is: its item, tile and half
+      struct Place {
+        int item, tile, s, tn, in;   // in: items before it
+      };
+      auto next = [&](Place p) {
+        if (p.s == 0) {
+          p.s = 1;
+          return p;
+        }
+        p.s = 0;
+        ++p.tn;
+        if (++p.tile >= last_tile(p.item)) {
+          p.item += gridDim.x;
+          ++p.in;
+          p.tile = p.item < items ? first_tile(p.item) : 0;
+        }
+        return p;
+      };
+      auto product = [&](const Place& p, int u) {   // D of slot u
+        if (p.s == 0 && p.tile == first_tile(p.item)) {
+          if (p.in > 0) wait(wempty, p.in - 1);
+          mbar_arrive_expect_tx(wfull, 2u * W_SLOT);
+          const uint8_t* w = P.wT + static_cast<size_t>(p.item % nblocks) * 2 * W_SLOT;
+          for (int s = 0; s < 2; ++s) {
+            bulk_load_hint(sm + SO_WHM + s * W_HM, w + s * W_SLOT, W_HM, wfull, wpol);
+            bulk_load_hint(sm + SO_WLO + s * W_LO, w + s * W_SLOT + W_HM, W_LO, wfull, wpol);
+          }
+          wait(wfull, p.in);
+        }
+        const int pb = p.tn & 1, db = u & 1;
+        if (p.s == 0) wait(&pfull[pb], p.tn >> 1);
+        if (u >= 2) wait(&dfree[db], (u >> 1) - 1);
+        tc_fence_after();
+        const uint32_t ahm = smem_u32(sm + SO_PHM + pb * SB_PHM), alo = smem_u32(sm + SO_PLO + pb * SB_PLO);
+        const uint32_t bhm = smem_u32(sm + SO_WHM + p.s * W_HM), blo = smem_u32(sm + SO_WLO + p.s * W_LO);
+        auto a_of = [&](int pl, int kk) {
+          return pl == 2 ? sdesc_kmajor_swizzled(alo + 32 * kk, 64) : sdesc_kmajor_swizzled(ahm + 64 * pl + 32 * kk, 128);
+        };
+        auto b_of = [&](int pl, int kk) {
+          return pl == 2 ? sdesc_kmajor_swizzled(blo + 32 * kk, 64) : sdesc_kmajor_swizzled(bhm + 64 * pl + 32 * kk, 128);
+        };
+        uint32_t more = 0;
+#pragma unroll
+        for (int sum = 2; sum >= 0; --sum)   // the smallest products first
+#pragma unroll
+          for (int pa = 0; pa <= sum; ++pa)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+              umma_bf16(tmem + static_cast<uint32_t>(db * 128), a_of(pa, kk), b_of(sum - pa, kk), id_d, more);
+              more = 1;
+            }
+        umma_commit(&dready[db]);
+        if (p.s == 1 && p.tile == last_tile(p.item) - 1) umma_commit(wempty);
+      };
+      Place cur{static_cast<int>(blockIdx.x), 0, 0, 0, 0};
+      if (cur.item < items) {
+        cur.tile = first_tile(cur.item);
+        product(cur, 0);
+      }
+      for (int u = 0; cur.item < items; ++u) {
+        const Place nx = next(cur);
+        if (nx.item < items) product(nx, u + 1);
+        // gW += X'^T (r g_m) of slot u
+        wait(xready, u);
+        const bool start = cur.tile == first_tile(cur.item);
+        if (start && cur.s == 0 && cur.in > 0) wait(gwfree, cur.in - 1);
+        tc_fence_after();
+        const int pb = cur.tn & 1;
+        const uint32_t xa = smem_u32(sm + SO_XP);
+        const uint32_t phm = smem_u32(sm + SO_PHM + pb * SB_PHM), plo = smem_u32(sm + SO_PLO + pb * SB_PLO);
+        const uint32_t acc = tmem + 256u + 96u * static_cast<uint32_t>(cur.s);
+        for (int ks = 0; ks < tt / 16; ++ks) {
+          const uint64_t a = sdesc_mnmajor(xa + ks * 1024, 64, SB_TILE, 512);
+          const uint32_t more = (start && ks == 0) ? 0u : 1u;
+          umma_bf16(acc, a, sdesc_mnmajor(phm + ks * 2048, 128, 0, 1024), id_hm, more);
+          umma_bf16(acc + 64, a, sdesc_mnmajor(plo + ks * 1024, 64, 0, 512), id_lo, more);
+        }
+        umma_commit(xfree);
+        if (cur.s == 1) umma_commit(&pempty[pb]);
+        if (cur.s == 1 && cur.tile == last_tile(cur.item) - 1) umma_commit(gwfull);
+        cur = nx;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ consumers
+    const int sub = warp & 3;            // TMEM lane quarter
+    const int h = (warp - 2) >> 2;       // which 16 columns of the slot
+    const int tl = sub * 32 + lane;      // token row of the tile
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+    // Threads past the tiles' height read the first row and write nothing.
+    const bool inrows = tl < SBR;
+    const int tr = inrows ? tl : 0;
+    auto row_off = [&](int q) { return tile_chunk_offset(tr, 2 * h + q); };
+    const uint32_t code_off = swizzled_chunk_offset(tr, h, 32);
+    const f2 nz{P.neg_zero, P.neg_zero};
+    const int nb = P.d / MX_BLOCK;
+    int u = 0, in = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x, ++in) {
+      const int cb = item % nblocks;
+      const int tile_end = last_tile(item);
+      for (int tile = first_tile(item); tile < tile_end; ++tile) {
+        const int token = tile * tt + tl;
+        const bool valid = tl < tt && token < P.N;
+        const size_t row = valid ? static_cast<size_t>(token) : 0;
+        // cc[j][k] = weight of input stream j in output stream k
+        f2 cc[4][4], cu[4], cpp[4];
+        f2 r_y2, tau2, c12;
+        uint32_t xs[4], fs;   // this item's two scale codes of each row
+        {
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+          auto ld = [&](const float* p, size_t i) { return valid ? __ldg(reinterpret_cast<const float4*>(p) + i) : zero; };
+          const float4 c0 = ld(P.comb, row * 4), c1 = ld(P.comb, row * 4 + 1), c2 = ld(P.comb, row * 4 + 2),
+                       c3 = ld(P.comb, row * 4 + 3);
+          const float4 uv = ld(P.post, row), pv = ld(P.pre, row), rv = ld(P.rec, row);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            xs[k] = valid ? __ldg(reinterpret_cast<const uint16_t*>(P.Xs + (row * 4 + k) * nb) + cb) : 0u;
+          fs = valid ? __ldg(reinterpret_cast<const uint16_t*>(P.Fs + row * nb) + cb) : 0u;
+          const float cm[16] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w,
+                                c2.x, c2.y, c2.z, c2.w, c3.x, c3.y, c3.z, c3.w};
+          const float uu[4] = {uv.x, uv.y, uv.z, uv.w}, pp[4] = {pv.x, pv.y, pv.z, pv.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            cu[k] = f2{uu[k], uu[k]};
+            cpp[k] = f2{pp[k], pp[k]};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float w = P.row_dest ? cm[4 * k + j] : cm[4 * j + k];
+              cc[j][k] = f2{w, w};
+            }
+          }
+          r_y2 = f2{rv.y, rv.y};
+          tau2 = f2{-rv.z, -rv.z};
+          c12 = f2{-rv.w, -rv.w};
+        }
+        float acc_u[4], acc_c[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc_u[k] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc_c[j][k] = 0.f;
+        }
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s, ++u) {
+          const int e = u & 1;
+          uint8_t* codes = sm + SO_C + e * SB_CODES;
+          uint8_t* bt = sm + SO_B + e * SB_SET;
+          wait(&cfull[e], u >> 1);
+          wait(&bfull[e], u >> 1);
+          wait(&dready[e], u >> 1);
+          if (u > 0) wait(xfree, u - 1);
+          tc_fence_after();
+          float sx[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sx[k] = scale_value((xs[k] >> (8 * s)) & 0xffu);
+          const float sf = scale_value((fs >> (8 * s)) & 0xffu);
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            uint2 xc[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) xc[k] = *reinterpret_cast<const uint2*>(codes + k * SB_CODE + code_off + 8 * q);
+            const uint2 fc = *reinterpret_cast<const uint2*>(codes + 4 * SB_CODE + code_off + 8 * q);
+            // gXp and gy, then gX and gF in their place
+            uint32_t ga[4][4], ya[4], xw[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint4 g = *reinterpret_cast<const uint4*>(bt + k * SB_TILE + row_off(q));
+              ga[k][0] = g.x; ga[k][1] = g.y; ga[k][2] = g.z; ga[k][3] = g.w;
+            }
+            {
+              const uint4 y = *reinterpret_cast<const uint4*>(bt + 4 * SB_TILE + row_off(q));
+              ya[0] = y.x; ya[1] = y.y; ya[2] = y.z; ya[3] = y.w;
+            }
+#pragma unroll
+            for (int hq = 0; hq < 2; ++hq) {
+              // W^T (r g_m) of 4 columns of each stream
+              uint32_t gw[4][4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tmem_ld_x4_nowait(lane_base + static_cast<uint32_t>(e * 128 + k * 32 + 16 * h + 8 * q + 4 * hq), gw[k]);
+              const float4 g0 = __ldg(reinterpret_cast<const float4*>(P.gain + cb * SB_COLS + 32 * s + 16 * h + 8 * q + 4 * hq));
+              const f2 gn[2] = {f2{g0.x, g0.y}, f2{g0.z, g0.w}};
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int w = 2 * hq + i;
+                auto word = [&](uint2 v) { return (hq == 0 ? v.x : v.y) >> (16 * i); };
+                const f2 f = decode2(word(fc), f2{sf, sf});
+                f2 x[4], xp[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = decode2(word(xc[j]), f2{sx[j], sx[j]});
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const f2 ck[4] = {cc[0][k], cc[1][k], cc[2][k], cc[3][k]};
+                  xw[k][w] = f2_to_bf2(hc_post_pair(ck, cu[k], x, f, nz));
+                  xp[k] = bf2_to_f2(xw[k][w]);
+                }
+                const f2 yh = bf2_to_f2(f2_to_bf2(hc_pre_pair(cpp, xp, nz)));
+                const f2 gyh = fma2(mul2(r_y2, gn[i]), bf2_to_f2(ya[w]), mul2(tau2, yh));
+                f2 G[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const f2 gmix{__uint_as_float(gw[k][2 * i]), __uint_as_float(gw[k][2 * i + 1])};
+                  f2 v = fma2(cpp[k], gyh, bf2_to_f2(ga[k][w]));
+                  v = add2(v, gmix);
+                  G[k] = fma2(c12, xp[k], v);
+                  acc_u[k] = fmaf(G[k].x, f.x, fmaf(G[k].y, f.y, acc_u[k]));
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    acc_c[j][k] = fmaf(G[k].x, x[j].x, fmaf(G[k].y, x[j].y, acc_c[j][k]));
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  f2 v = mul2(cc[j][0], G[0]);
+                  v = fma2(cc[j][1], G[1], v);
+                  v = fma2(cc[j][2], G[2], v);
+                  v = fma2(cc[j][3], G[3], v);
+                  ga[j][w] = f2_to_bf2(v);
+                }
+                f2 vf = mul2(cu[0], G[0]);
+                vf = fma2(cu[1], G[1], vf);
+                vf = fma2(cu[2], G[2], vf);
+                vf = fma2(cu[3], G[3], vf);
+                ya[w] = f2_to_bf2(vf);
+              }
+            }
+            if (inrows) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                *reinterpret_cast<uint4*>(sm + SO_XP + k * SB_TILE + row_off(q)) =
+                    make_uint4(xw[k][0], xw[k][1], xw[k][2], xw[k][3]);
+                *reinterpret_cast<uint4*>(bt + k * SB_TILE + row_off(q)) =
+                    make_uint4(ga[k][0], ga[k][1], ga[k][2], ga[k][3]);
+              }
+              *reinterpret_cast<uint4*>(bt + 4 * SB_TILE + row_off(q)) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
+            }
+          }
+          tc_fence_before();   // the TMEM loads above, before the MMA that reuses the buffer
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&dfree[e]);
+            mbar_arrive(xready);
+            mbar_arrive(&gready[e]);
+            if (s == 0) mbar_arrive(&cempty[e]);
+          }
+        }
+        // gu and gC of the item's columns: the second thread's sums through the codes' rows of this token,
+        // which both threads have read
+        {
+          const int e = (u - 1) & 1;
+          uint8_t* codes = sm + SO_C + e * SB_CODES + swizzled_chunk_offset(tr, 0, 32);
+          named_bar_sync(1 + sub, 64);
+          if (h == 1 && inrows) {
+            *reinterpret_cast<float4*>(codes) = make_float4(acc_u[0], acc_u[1], acc_u[2], acc_u[3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4*>(codes + (1 + j) * SB_CODE) =
+                  make_float4(acc_c[j][0], acc_c[j][1], acc_c[j][2], acc_c[j][3]);
+          }
+          named_bar_sync(1 + sub, 64);
+          if (h == 0 && valid) {
+            float4* out = reinterpret_cast<float4*>(P.part_t + (static_cast<size_t>(cb) * P.N + token) * 20);
+            const float4 a = *reinterpret_cast<const float4*>(codes);
+            out[0] = make_float4(acc_u[0] + a.x, acc_u[1] + a.y, acc_u[2] + a.z, acc_u[3] + a.w);
+            float o[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 b = *reinterpret_cast<const float4*>(codes + (1 + j) * SB_CODE);
+              o[j][0] = acc_c[j][0] + b.x;
+              o[j][1] = acc_c[j][1] + b.y;
+              o[j][2] = acc_c[j][2] + b.z;
+              o[j][3] = acc_c[j][3] + b.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              out[1 + i] = P.row_dest ? make_float4(o[0][i], o[1][i], o[2][i], o[3][i])
+                                      : make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+          }
+          fence_proxy_async_smem();   // these accesses, before the copy that refills the codes
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&cempty[e]);
+        }
+      }
+      // gW of the item: accumulator h holds (stream sub, column 32 h + lane of the block) in this lane's row,
+      // mix row o's three plane sums in columns o, 32 + o, 64 + o
+      wait(gwfull, in);
+      tc_fence_after();
+      {
+        const uint32_t acc = lane_base + 256u + 96u * static_cast<uint32_t>(h);
+        uint32_t a[32], b[32], l[32];
+        tmem_ld_x32(acc, a);
+        tmem_ld_x32(acc + 32, b);
+        tmem_ld_x32(acc + 64, l);
+        float* pw = P.part_w + static_cast<size_t>(item / nblocks) * MIXN * 4 * P.d +
+                    static_cast<size_t>(sub) * P.d + cb * SB_COLS + 32 * h + lane;
+#pragma unroll
+        for (int o = 0; o < MIXN; ++o)
+          pw[static_cast<size_t>(o) * 4 * P.d] =
+              __uint_as_float(a[o]) + (__uint_as_float(b[o]) + __uint_as_float(l[o]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(gwfree);
+    }
+  }
+
+  if (timed_out) atomicOr(P.status, STATUS_TIMEOUT);
+  tc_fence_before();
+  block_sync();
+  if (warp == 1) tmem_dealloc(tmem, SB_TMEM);
+}
+
+// ---------------------------------------------------------------------------------------------
+// ckb_reduce_kernel: float4 sums of partials in their order. Blocks [0, gw) sum gW over the ranges,
+// [gw, gw + gg) ggain over the token kernel's blocks (8 threads an output), [.., + gt) gu and gC of the tokens
+// over the column blocks, and the last one g_base and g_scale.
+struct ReduceParams {
+  const float* part_w;
+  const float* part_gain;
+  const float* part_t;
+  const float* part_mix;
+  float* gW;
+  float* ggain;
+  float* gpost;
+  float* gcomb;
+  float* gbase;
+  float* gscale;
+  int64_t N;
+  int d;
+  int ranges, gain_rows, mix_blocks;
+  int gw, gg;
+  int64_t gt;
+};
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__global__ void __launch_bounds__(256) ckb_reduce_kernel(const ReduceParams P) {
+  __shared__ float4 red[8][32];
+  const int64_t blk = blockIdx.x;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (blk < P.gw) {
+    const int64_t n4 = static_cast<int64_t>(MIXN) * P.d, i = blk * 256 + threadIdx.x;
+    if (i >= n4) return;
+    float4 v = zero;
+#pragma unroll 4
+    for (int r = 0; r < P.ranges; ++r) v = add4(v, __ldg(reinterpret_cast<const float4*>(P.part_w) + r * n4 + i));
+    reinterpret_cast<float4*>(P.gW)[i] = v;
+  } else if (blk < P.gw + P.gg) {
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int n4 = P.d / 4;
+    const int64_t i = (blk - P.gw) * 32 + lane;
+    float4 v = zero;
+    if (i < n4)
+#pragma unroll 4
+      for (int r = g; r < P.gain_rows; r += 8)
+        v = add4(v, __ldg(reinterpret_cast<const float4*>(P.part_gain) + static_cast<int64_t>(r) * n4 + i));
+    red[g][lane] = v;
+    __syncthreads();
+    if (g != 0 || i >= n4) return;
+    v = zero;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v = add4(v, red[k][lane]);
+    reinterpret_cast<float4*>(P.ggain)[i] = v;
+  } else if (blk < P.gw + P.gg + P.gt) {
+    const int64_t n4 = P.N * 5, i = (blk - P.gw - P.gg) * 256 + threadIdx.x;
+    if (i >= n4) return;
+    float4 v = zero;
+    const int nblocks = P.d / SB_COLS;
+#pragma unroll 8
+    for (int b = 0; b < nblocks; ++b) v = add4(v, __ldg(reinterpret_cast<const float4*>(P.part_t) + b * n4 + i));
+    const int64_t t = i / 5;
+    const int q = static_cast<int>(i - 5 * t);
+    if (q == 0) reinterpret_cast<float4*>(P.gpost)[t] = v;
+    else reinterpret_cast<float4*>(P.gcomb)[t * 4 + q - 1] = v;
+  } else {
+    float* f = reinterpret_cast<float*>(red);
+    const int j = threadIdx.x & 31, q = threadIdx.x >> 5;
+    float v = 0.f;
+    if (j < MIXN + 3)
+      for (int b = q; b < P.mix_blocks; b += 8) v += __ldg(P.part_mix + static_cast<int64_t>(b) * 32 + j);
+    f[q * 32 + j] = v;
+    __syncthreads();
+    if (threadIdx.x >= MIXN + 3) return;
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v += f[k * 32 + threadIdx.x];
+    if (threadIdx.x < MIXN) P.gbase[threadIdx.x] = v;
+    else P.gscale[threadIdx.x - MIXN] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// host side
+
+// Byte offsets of the workspace's parts and the work split.
+struct Plan {
+  size_t wt, gm, rec, hm, lo, mix, gain, w, t, bytes;
+  int tt, ntiles, per, ranges;   // stream kernel
+  int mix_blocks, gain_rows;
+};
+
+// Token tiles of tt rows in `ranges` ranges of `per` tiles: the busiest block's items x tiles x time of a
+// tile, which is about that of its tokens and 40 more (waits and fills that every slot has).
+Plan plan_of(int64_t N, int d, int sms) {
+  Plan p{};
+  if (sms <= 0 || d <= 0 || d % SB_COLS != 0) return p;
+  const int64_t nblocks = d / SB_COLS;
+  int64_t best = INT64_MAX;
+  p.tt = 16;
+  p.ntiles = p.per = p.ranges = 1;
+  for (int tt = SBR; N > 0 && tt >= 16; tt -= 16) {
+    const int64_t tiles = (N + tt - 1) / tt;
+    const int64_t most = std::min<int64_t>(tiles, 64);
+    for (int64_t want = 1; want <= most; ++want) {
+      const int64_t per = (tiles + want - 1) / want, ranges = (tiles + per - 1) / per;
+      const int64_t rounds = (nblocks * ranges + sms - 1) / sms;
+      // a range costs its W^T load and its gW sums, about a tile of 32 tokens
+      const int64_t cost = rounds * (per * (tt + 40) + 32);
+      if (cost < best) {
+        best = cost;
+        p.tt = tt;
+        p.ntiles = static_cast<int>(tiles);
+        p.per = static_cast<int>(per);
+        p.ranges = static_cast<int>(ranges);
+      }
+    }
+  }
+  p.mix_blocks = static_cast<int>((N + PREP_TOKENS - 1) / PREP_TOKENS);
+  p.gain_rows = static_cast<int>(std::min<int64_t>(std::max<int64_t>(N, 1), 2 * static_cast<int64_t>(sms)));
+  size_t off = 0;
+  auto part = [&](size_t bytes) {
+    const size_t at = off;
+    off += a256(bytes);
+    return at;
+  };
+  const size_t n = static_cast<size_t>(N);
+  p.wt = part(static_cast<size_t>(d / 32) * W_SLOT);
+  p.gm = part(n * MIXN * 4);
+  p.rec = part(n * 16);
+  p.hm = part(n * 128);
+  p.lo = part(n * 64);
+  p.mix = part(static_cast<size_t>(p.mix_blocks) * 128);
+  p.gain = part(static_cast<size_t>(p.gain_rows) * d * 4);
+  p.w = part(static_cast<size_t>(p.ranges) * MIXN * 4 * d * 4);
+  p.t = part(static_cast<size_t>(nblocks) * n * 80);
+  p.bytes = off;
+  return p;
+}
+
+// Codes: uint8 [rows][4 or 1][d], boxes of 32 columns of `rows_box` rows, 32-byte swizzle.
+bool code_map(CUtensorMap* m, const void* p, int64_t N, int d, int streams, uint32_t rows_box) {
+  auto fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const cuuint64_t D = static_cast<cuuint64_t>(d), n = static_cast<cuuint64_t>(N);
+  const cuuint64_t dims3[3] = {D, 4, n}, str3[2] = {D, 4 * D}, dims2[2] = {D, n}, str2[1] = {D};
+  const cuuint32_t box3[3] = {32, 1, rows_box}, box2[2] = {32, rows_box}, estr[3] = {1, 1, 1};
+  const bool three = streams == 4;
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, three ? 3 : 2, const_cast<void*>(p), three ? dims3 : dims2,
+            three ? str3 : str2, three ? box3 : box2, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+size_t bwd_ckpt_bytes(int64_t N, int d) { return plan_of(N, d, sm_count()).bytes; }
+
+cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cudaStream_t stream) {
+  const int sms = sm_count(), d = a.d;
+  const int64_t N = a.N;
+  const Plan p = plan_of(N, d, sms);
+  if (p.bytes == 0 || a.workspace_bytes < p.bytes) return cudaErrorInvalidValue;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  auto wsf = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  unsigned* status = status_word();
+  if (status == nullptr) return cudaErrorInvalidDevice;
+  const int row_dest = static_cast<int>(a.flags & 1u);
+  cudaError_t e;
+  {
+    const int steps = 2 * a.iters - 1, every = (steps + PREP_KEEP - 1) / PREP_KEEP;
+    const int smem = (steps + every - 1) / every * PREP_THREADS * 16;
+    if (smem > 48 * 1024 - 1024) {
+      e = cudaFuncSetAttribute(ckb_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+    }
+    ckb_prep_kernel<<<p.mix_blocks + d / 32, PREP_THREADS, smem, stream>>>(
+        a.mixes, a.gpre, a.gpost, a.gcomb, a.scale, a.base, a.W, wsf(p.gm), wsf(p.mix), ws + p.wt, N, d, a.iters,
+        a.hc_eps, p.mix_blocks, every);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  {
+    const CkIn in{static_cast<const uint2*>(ck.X_codes), static_cast<const uint8_t*>(ck.X_scale),
+                  static_cast<const uint2*>(ck.F_codes), static_cast<const uint8_t*>(ck.F_scale)};
+    auto run = [&](auto kernel, int ch) {
+      const int threads = ((d / 8 + ch - 1) / ch + 31) / 32 * 32;
+      kernel<<<p.gain_rows, threads, 0, stream>>>(
+          in, static_cast<const uint4*>(a.gy), a.pre_prev, a.post_prev, a.comb_prev, a.gain, a.mixes, wsf(p.gm),
+          wsf(p.rec), reinterpret_cast<__nv_bfloat16*>(ws + p.hm), reinterpret_cast<__nv_bfloat16*>(ws + p.lo),
+          a.gpre_prev, wsf(p.gain), N, d, a.norm_eps, row_dest, -0.0f);
+      return cudaGetLastError();
+    };
+    const int chunks = d / 8, most = TOKEN_WARPS * 32;
+    e = chunks <= most ? run(ckb_token_kernel<1>, 1)
+        : chunks <= 2 * most ? run(ckb_token_kernel<2>, 2)
+        : chunks <= 4 * most ? run(ckb_token_kernel<4>, 4)
+                             : run(ckb_token_kernel<8>, 8);
+    if (e != cudaSuccess) return e;
+  }
+  {
+    const uint32_t tt = static_cast<uint32_t>(p.tt);
+    CUtensorMap tx, tf, tgxp, tgy, tgx, tgf, thm, tlo;
+    if (!code_map(&tx, ck.X_codes, N, d, 4, tt) || !code_map(&tf, ck.F_codes, N, d, 1, tt) ||
+        !bmap_streams(&tgxp, a.gXp, N, d, tt) || !bmap_rows(&tgy, a.gy, N, d, 32, tt, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !bmap_streams(&tgx, a.gX, N, d, tt) || !bmap_rows(&tgf, a.gF, N, d, 32, tt, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !bmap_rows(&thm, ws + p.hm, N, 64, 64, tt, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !bmap_rows(&tlo, ws + p.lo, N, 32, 32, tt, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+    SbParams P{};
+    P.pre = a.pre_prev;
+    P.post = a.post_prev;
+    P.comb = a.comb_prev;
+    P.rec = wsf(p.rec);
+    P.gain = a.gain;
+    P.Xs = static_cast<const uint8_t*>(ck.X_scale);
+    P.Fs = static_cast<const uint8_t*>(ck.F_scale);
+    P.wT = ws + p.wt;
+    P.part_w = wsf(p.w);
+    P.part_t = wsf(p.t);
+    P.status = status;
+    P.N = static_cast<int>(N);
+    P.d = d;
+    P.tt = p.tt;
+    P.ntiles = p.ntiles;
+    P.per = p.per;
+    P.ranges = p.ranges;
+    P.neg_zero = -0.0f;
+    P.row_dest = row_dest;
+    e = cudaFuncSetAttribute(ckb_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SB_SMEM);
+    if (e != cudaSuccess) return e;
+    const int items = d / SB_COLS * p.ranges;
+    ckb_stream_kernel<<<std::min(items, sms), SB_THREADS, SB_SMEM, stream>>>(tx, tf, tgxp, tgy, tgx, tgf, thm, tlo, P);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  ReduceParams R{};
+  R.part_w = wsf(p.w);
+  R.part_gain = wsf(p.gain);
+  R.part_t = wsf(p.t);
+  R.part_mix = wsf(p.mix);
+  R.gW = a.gW;
+  R.ggain = a.ggain;
+  R.gpost = a.gpost_prev;
+  R.gcomb = a.gcomb_prev;
+  R.gbase = a.gbase;
+  R.gscale = a.gscale;
+  R.N = N;
+  R.d = d;
+  R.ranges = p.ranges;
+  R.gain_rows = p.gain_rows;
+  R.mix_blocks = p.mix_blocks;
+  R.gw = (MIXN * d + 255) / 256;
+  R.gg = (d / 4 + 31) / 32;
+  R.gt = (N * 5 + 255) / 256;
+  ckb_reduce_kernel<<<static_cast<unsigned>(R.gw + R.gg + R.gt + 1), 256, 0, stream>>>(R);
+  return cudaGetLastError();
+}
+
+}  // namespace mhc

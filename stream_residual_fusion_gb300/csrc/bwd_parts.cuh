@@ -1,0 +1,83 @@
+// bwd_parts.cuh -- what the two backward paths of the fused step share (backward.cu: from X, F and X';
+// backward_ckpt.cu: from checkpoints): operand descriptors, small arithmetic and tensor maps.
+#pragma once
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "layout.cuh"
+#include "ptx.cuh"
+
+namespace mhc {
+namespace {
+
+constexpr int MIXN = 24;
+constexpr uint64_t BWD_WAIT_NS = 2000000000ull;   // 2 s
+
+// Reciprocal of a positive normal float within 1 ulp (the hardware approximation).
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float sigmoid_b(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// Shared-memory descriptor of an MN-major operand: `row_bytes` (64 or 128) of the MN dimension
+// per row with the swizzle of that width, consecutive K rows row_bytes apart, 8-row K groups
+// `sbo` bytes apart, the next MN atom `lbo` bytes on.
+__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t saddr, int row_bytes, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(row_bytes == 128 ? 2 : 4) << 61);
+}
+
+// No L2 promotion: a CTA of these kernels reads the neighbouring columns of a row only slots
+// later, so fetching them early only adds traffic.
+inline bool bmap(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+          const cuuint32_t* box, CUtensorMapSwizzle swz) {
+  auto fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool bmap_streams(CUtensorMap* m, const void* p, int64_t N, int d, uint32_t rows) {   // [N, 4, d], boxes of 32 columns
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), 4, static_cast<cuuint64_t>(N)};
+  const cuuint64_t str[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(d) * 8};
+  const cuuint32_t box[3] = {32, 1, rows};
+  return bmap(m, p, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+inline bool bmap_streams_box(CUtensorMap* m, const void* p, int64_t N, int d, uint32_t cols, uint32_t rows,
+                      CUtensorMapSwizzle swz) {   // [N, 4, d], boxes of [rows x cols] of one stream
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), 4, static_cast<cuuint64_t>(N)};
+  const cuuint64_t str[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(d) * 8};
+  const cuuint32_t box[3] = {cols, 1, rows};
+  return bmap(m, p, 3, dims, str, box, swz);
+}
+inline bool bmap_rows(CUtensorMap* m, const void* p, int64_t N, int cols, uint32_t box_cols, uint32_t rows,
+               CUtensorMapSwizzle swz) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(N)};
+  const cuuint64_t str[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t box[2] = {box_cols, rows};
+  return bmap(m, p, 2, dims, str, box, swz);
+}
+
+inline int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+inline int gcd_i(int a, int b) { return b == 0 ? a : gcd_i(b, a % b); }
+
+inline size_t a256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace mhc
