@@ -246,8 +246,8 @@ size_t mhc_checkpoint_scale_bytes(int64_t rows, int d);
  * mhc_checkpoint_save writes the N n rows of X, F_codes [N, d] and F_scale [N, d / 32]) and without
  * X'. The decoded values stand in for X and F, X' = hc_post of them in the forward's float32
  * arithmetic, rounded to bf16, y_hat = hc_pre(X') rounded to bf16; mixes is the forward's m, whose
- * gradient g_m is that of the forward. d a multiple of 64, at most 24576. All else as there, but four
- * kernels, and the sums over tokens in float32 throughout (three bf16 planes of r g_m and of W).
+ * gradient g_m is that of the forward. All else as there, but in four kernels, with r g_m and W held
+ * to float32's accuracy in three bf16 planes each.
  * workspace: >= mhc_backward_ckpt_workspace_bytes(N, n, d) device bytes, 16-byte aligned.      */
 int mhc_fused_step_backward_ckpt(const void* X_codes, const void* X_scale, const void* F_codes,
                                  const void* F_scale, const float* mixes, const float* pre_prev,

@@ -160,7 +160,6 @@ int backward_common(const BwdArgs& a, int n, const BwdCheckpoint* c, void* strea
   const int64_t N = a.N;
   const int d = a.d;
   if (n != 4 || N < 0 || N > kMaxTokens || d <= 0 || d % 64 != 0 || a.iters < 1) return MHC_ERR_SHAPE;
-  if (c && d > kCkptMaxWidth) return MHC_ERR_SHAPE;
   if ((a.flags & ~MHC_COMB_ROW_DEST) != 0) return MHC_ERR_SHAPE;
   if (!a.W || !a.scale || !a.base || !a.gain || !a.gW || !a.gbase || !a.gscale || !a.ggain) return MHC_ERR_NULL;
   const void* params[] = {a.W, a.scale, a.base, a.gain, a.gW, a.gbase, a.gscale, a.ggain};
@@ -682,7 +681,7 @@ int mhc_fused_step_backward(const void* X, const void* F, const void* Xp, const 
 }
 
 size_t mhc_backward_ckpt_workspace_bytes(int64_t N, int n, int d) {
-  if (n != 4 || N < 0 || N > kMaxTokens || d <= 0 || d % 64 != 0 || d > kCkptMaxWidth) return 0;
+  if (n != 4 || N < 0 || N > kMaxTokens || d <= 0 || d % 64 != 0) return 0;
   return bwd_ckpt_bytes(N, d);
 }
 

@@ -7,9 +7,9 @@
 // Four launches on the caller's stream:
 //   ckb_prep_kernel    the split's and Sinkhorn's derivatives (g_m), four lanes a token, one row of the
 //                      4 x 4 matrix each; beside them, in blocks of their own, the bf16 planes of W^T.
-//   ckb_token_kernel   one block a token: the sums over its width that give r, r_y, tau, c1 and gp, the
-//                      three bf16 planes of r g_m, and ggain, which gathers in the threads' registers.
-//   ckb_stream_kernel  work items of (64 columns of every stream, a range of token tiles): gX, gF, and
+//   ckb_token_kernel   one warp or one block a token: the sums over its width that give r, r_y, tau, c1 and gp, the
+//                      three bf16 planes of r g_m.
+//   ckb_stream_kernel  work items of (64 columns of every stream, a range of token tiles): gX, gF, ggain and
 //                      gW, for which X' never leaves the SM (below).
 //   ckb_reduce_kernel  sums of partials in a fixed order: gW, ggain, g_base, g_scale, and gu, gC of every
 //                      token over the column blocks.
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(PREP_THREADS) ckb_prep_kernel(
 // ---------------------------------------------------------------------------------------------
 // ckb_token_kernel
 
-constexpr int TOKEN_WARPS = 12;     // warps of a block, at most
+constexpr int TOKEN_WARPS = 8;
 
 struct CkIn {
   const uint2* X;          // codes [N, 4, d], 8 to a word pair
@@ -225,117 +225,113 @@ struct CkIn {
   const uint8_t* Fs;
 };
 
-template <int CH>
-__global__ void __launch_bounds__(TOKEN_WARPS * 32) ckb_token_kernel(
+// WPT warps a token: one where there are enough tokens to fill the device, else the whole block.
+template <int WPT>
+__global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
     const CkIn in, const uint4* __restrict__ gy, const float* __restrict__ pre, const float* __restrict__ post,
     const float* __restrict__ comb, const float* __restrict__ gain, const float* __restrict__ mixes,
     const float* __restrict__ gm, float* __restrict__ rec, __nv_bfloat16* __restrict__ planes_hm,
-    __nv_bfloat16* __restrict__ planes_lo, float* __restrict__ gpre_prev, float* __restrict__ part_gain,
-    int64_t N, int d, float norm_eps, int row_dest, float neg_zero) {
-  // |x|^2, |y_hat|^2, T, gain gy . X'_j, y_hat . X'_j
-  constexpr int V = 16;
+    __nv_bfloat16* __restrict__ planes_lo, float* __restrict__ gpre_prev, int64_t N, int d, float norm_eps,
+    int row_dest, float neg_zero) {
+  constexpr int V = 16;   // |x|^2, |y_hat|^2, T, gain gy . X'_j, y_hat . X'_j
   __shared__ float scratch[2][TOKEN_WARPS * V];
-  const int T = blockDim.x, warps = T / 32, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = d / 8, blocks = d / MX_BLOCK;
   const f2 nz{neg_zero, neg_zero};
   const float fd = static_cast<float>(d), fk = 4.0f * fd;
-  f2 sum_gain[CH][4];
-#pragma unroll
-  for (int q = 0; q < CH; ++q)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum_gain[q][i] = f2{0.f, 0.f};
+  constexpr int TPB = TOKEN_WARPS / WPT;   // tokens of a block at a time
+  const int64_t step = static_cast<int64_t>(gridDim.x) * TPB;
   int n = 0;
-  for (int64_t t = blockIdx.x; t < N; t += gridDim.x, ++n) {
-    uint2 xc[CH][4], fc[CH];
-    uint32_t xs[CH], fs[CH];
-    uint4 gyw[CH];
-#pragma unroll
-    for (int q = 0; q < CH; ++q) {
-      const int c = static_cast<int>(threadIdx.x) + q * T;
-      if (c >= chunks) break;
-      xs[q] = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        xc[q][k] = __ldg(in.X + (t * 4 + k) * chunks + c);
-        xs[q] |= static_cast<uint32_t>(__ldg(in.Xs + (t * 4 + k) * blocks + c / 4)) << (8 * k);
-      }
-      fc[q] = __ldg(in.F + t * chunks + c);
-      fs[q] = __ldg(in.Fs + t * blocks + c / 4);
-      gyw[q] = __ldg(gy + t * chunks + c);
-    }
+  for (int64_t t = blockIdx.x * static_cast<int64_t>(TPB) + warp / WPT; t < N; t += step, ++n) {
     float gmi = 0.f, mi = 0.f;
-    if (threadIdx.x < MIXN) {
-      gmi = __ldg(gm + t * MIXN + threadIdx.x);
-      mi = __ldg(mixes + t * MIXN + threadIdx.x);
+    if (lane < MIXN) {
+      gmi = __ldg(gm + t * MIXN + lane);
+      mi = __ldg(mixes + t * MIXN + lane);
     }
     f2 cc[4][4], cu[4], cp[4];
+    {
+      const float4 u4 = __ldg(reinterpret_cast<const float4*>(post) + t), p4 = __ldg(reinterpret_cast<const float4*>(pre) + t);
+      const float uu[4] = {u4.x, u4.y, u4.z, u4.w}, pp[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float u = __ldg(post + t * 4 + k), p = __ldg(pre + t * 4 + k);
-      cu[k] = f2{u, u};
-      cp[k] = f2{p, p};
+      for (int i = 0; i < 4; ++i) {
+        const float4 c4 = __ldg(reinterpret_cast<const float4*>(comb) + t * 4 + i);
+        const float cm[4] = {c4.x, c4.y, c4.z, c4.w};
+        cu[i] = f2{uu[i], uu[i]};
+        cp[i] = f2{pp[i], pp[i]};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float w = __ldg(comb + t * 16 + (row_dest ? 4 * k + j : 4 * j + k));
-        cc[j][k] = f2{w, w};
+        for (int m = 0; m < 4; ++m) {
+          if (row_dest) cc[m][i] = f2{cm[m], cm[m]};
+          else cc[i][m] = f2{cm[m], cm[m]};
+        }
       }
     }
-    float v[V];
+    f2 acc[11];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.f;
-    auto dot = [&](int i, f2 a, f2 b) { v[i] = fmaf(a.x, b.x, fmaf(a.y, b.y, v[i])); };
-    f2 gyy[CH][4];   // gy y_hat, for ggain
+    for (int i = 0; i < 11; ++i) acc[i] = f2{0.f, 0.f};
+    const uint2* xr = in.X + t * 4 * chunks;
+    const uint8_t* xsr = in.Xs + t * 4 * blocks;
+    struct Raw {
+      uint2 x[4], f;
+      uint32_t s[5];
+      uint4 gy;
+    };
+    auto fetch = [&](int c, Raw& o) {
 #pragma unroll
-    for (int q = 0; q < CH; ++q) {
-      const int c = static_cast<int>(threadIdx.x) + q * T;
-      if (c >= chunks) break;
+      for (int k = 0; k < 4; ++k) {
+        o.x[k] = __ldg(xr + k * chunks + c);
+        o.s[k] = __ldg(xsr + k * blocks + c / 4);
+      }
+      o.f = __ldg(in.F + t * chunks + c);
+      o.s[4] = __ldg(in.Fs + t * blocks + c / 4);
+      o.gy = __ldg(gy + t * chunks + c);
+    };
+    // the next chunk's loads are issued before this one's arithmetic
+    Raw cur, nxt;
+    int c = (warp % WPT) * 32 + lane;
+    if (c < chunks) fetch(c, cur);
+    for (; c < chunks; c += 32 * WPT) {
+      if (c + 32 * WPT < chunks) fetch(c + 32 * WPT, nxt);
       const float4 g0 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * c);
       const float4 g1 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * c + 1);
       const f2 ga[4] = {f2{g0.x, g0.y}, f2{g0.z, g0.w}, f2{g1.x, g1.y}, f2{g1.z, g1.w}};
-      const uint32_t gw[4] = {gyw[q].x, gyw[q].y, gyw[q].z, gyw[q].w};
-      f2 sx[4], sf;
+      const uint32_t gw[4] = {cur.gy.x, cur.gy.y, cur.gy.z, cur.gy.w};
+      float sx[5];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float s = scale_value((xs[q] >> (8 * k)) & 0xffu);
-        sx[k] = f2{s, s};
-      }
-      const float s = scale_value(fs[q]);
-      sf = f2{s, s};
+      for (int k = 0; k < 5; ++k) sx[k] = scale_value(cur.s[k]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         auto word = [&](uint2 w) { return (i < 2 ? w.x : w.y) >> (16 * (i & 1)); };
         f2 x[4], xp[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = decode2(word(xc[q][k]), sx[k]);
-        const f2 f = decode2(word(fc[q]), sf);
+        for (int k = 0; k < 4; ++k) x[k] = decode2(word(cur.x[k]), f2{sx[k], sx[k]});
+        const f2 f = decode2(word(cur.f), f2{sx[4], sx[4]});
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const f2 ck[4] = {cc[0][k], cc[1][k], cc[2][k], cc[3][k]};
           xp[k] = bf2_to_f2(f2_to_bf2(hc_post_pair(ck, cu[k], x, f, nz)));
-          dot(0, xp[k], xp[k]);
+          acc[0] = fma2(xp[k], xp[k], acc[0]);
         }
         const f2 yh = bf2_to_f2(f2_to_bf2(hc_pre_pair(cp, xp, nz)));
-        const f2 g = bf2_to_f2(gw[i]);
-        const f2 gg = mul2(ga[i], g);
-        dot(1, yh, yh);
-        dot(2, gg, yh);
+        const f2 gg = mul2(ga[i], bf2_to_f2(gw[i]));
+        acc[1] = fma2(yh, yh, acc[1]);
+        acc[2] = fma2(gg, yh, acc[2]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          dot(3 + k, gg, xp[k]);
-          dot(7 + k, yh, xp[k]);
+          acc[3 + k] = fma2(gg, xp[k], acc[3 + k]);
+          acc[7 + k] = fma2(yh, xp[k], acc[7 + k]);
         }
-        gyy[q][i] = mul2(g, yh);
       }
+      cur = nxt;
     }
-    const float tot = group_sums<V>(v, scratch[n & 1], warps, T);
-    const float ry = __frsqrt_rn(__fdiv_rn(lane_value(tot, 1), fd) + norm_eps);
+    float v[V];
 #pragma unroll
-    for (int q = 0; q < CH; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (static_cast<int>(threadIdx.x) + q * T < chunks) sum_gain[q][i] = fma2(f2{ry, ry}, gyy[q][i], sum_gain[q][i]);
-    if (threadIdx.x < 32) {
+    for (int i = 0; i < V; ++i) v[i] = i < 11 ? acc[i].x + acc[i].y : 0.f;
+    float tot;   // lane l: the token's total of value l % 16
+    if constexpr (WPT == 1) tot = warp_sums<V>(v);
+    else tot = group_sums<V>(v, scratch[n & 1], TOKEN_WARPS, TOKEN_WARPS * 32);
+    if (warp % WPT == 0) {
       const float r = __frsqrt_rn(__fdiv_rn(lane_value(tot, 0), fk) + norm_eps);
+      const float ry = __frsqrt_rn(__fdiv_rn(lane_value(tot, 1), fd) + norm_eps);
       const float tau = ry * ry * ry * lane_value(tot, 2) / fd;
       float gmm = gmi * mi;
 #pragma unroll
@@ -350,31 +346,26 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32) ckb_token_kernel(
       if (lane == 0) reinterpret_cast<float4*>(rec)[t] = make_float4(r, ry, tau, c1);
     }
   }
-#pragma unroll
-  for (int q = 0; q < CH; ++q) {
-    const int c = static_cast<int>(threadIdx.x) + q * T;
-    if (c >= chunks) break;
-    float4* o = reinterpret_cast<float4*>(part_gain + blockIdx.x * static_cast<int64_t>(d)) + 2 * c;
-    o[0] = make_float4(sum_gain[q][0].x, sum_gain[q][0].y, sum_gain[q][1].x, sum_gain[q][1].y);
-    o[1] = make_float4(sum_gain[q][2].x, sum_gain[q][2].y, sum_gain[q][3].x, sum_gain[q][3].y);
-  }
 }
 
 // ---------------------------------------------------------------------------------------------
 // ckb_stream_kernel: per work item, W^T (r g_m) and gW on the tensor cores around the elementwise
-// gradients. A tile is up to 112 tokens; a slot is 32 columns of every stream of a tile.
-//   warp 0, lane 0   TMA loads: codes (2 slots ahead), gXp and gy (2 slots), the tile's planes of r g_m.
-//   warp 0, lane 1   TMA stores of gX, gF, which were written over gXp and gy.
-//   warp 1, lane 0   W^T of the item's columns, and the MMAs: D = A W^T^T for the next slot (A = the planes
+// gradients. A tile is up to 96 tokens; a slot is 32 columns of every stream of a tile.
+//   warp 3, lane 0   TMA loads: codes (2 slots ahead), gXp and gy (2 slots), the tile's planes of r g_m.
+//   warp 3, lane 1   TMA stores of gX, gF, which were written over gXp and gy.
+//   warp 7, lane 0   W^T of the item's columns, and the MMAs: D = A W^T^T for the next slot (A = the planes
 //                    [tokens x 24] of r g_m, six products of planes, the three largest orders), then
 //                    gW += X'^T A of this slot once the consumers have laid X' down.
-//   warps 2..9       two threads a token, 16 columns of the slot each.
+//   the others       two threads a token, 16 columns of the slot each, and ggain of those columns.
+// Eight warps leave each thread 255 registers, which its token's weights (as pairs), sums and operands take:
+// with ten (168 registers) what was spilled missed the little L1 beside 220 KB of shared memory, and a slot
+// took 7.7 us. Tiles of 96 tokens are the three TMEM lane quarters of the six consumer warps.
 
 constexpr int SBT = 128;                     // rows of D
-constexpr int SBR = 112;                     // token rows of a tile, at most
-constexpr int SB_CODE = SBR * 32;            // codes of one stream (or F): [112 x 32] bytes
+constexpr int SBR = 96;                      // token rows of a tile, at most
+constexpr int SB_CODE = SBR * 32;            // codes of one stream (or F): [96 x 32] bytes
 constexpr int SB_CODES = 5 * SB_CODE;
-constexpr int SB_TILE = SBR * 64;            // [112 x 32] bf16
+constexpr int SB_TILE = SBR * 64;            // [96 x 32] bf16
 constexpr int SB_SET = 5 * SB_TILE;
 constexpr int SB_PHM = SBR * 128;            // planes of r g_m: hi and mid
 constexpr int SB_PLO = SBR * 64;
@@ -382,7 +373,7 @@ constexpr int SO_PHM = 0;                    // two of each, then the item's W^T
 constexpr int SO_WHM = SO_PHM + 2 * SB_PHM;
 constexpr int SO_WLO = SO_WHM + 2 * W_HM;
 constexpr int SO_PLO = SO_WLO + 2 * W_LO;
-constexpr int SO_XP = SO_PLO + 2 * SB_PLO;   // X' of the slot, [112 x 32] bf16 of each stream
+constexpr int SO_XP = SO_PLO + 2 * SB_PLO;   // X' of the slot, [96 x 32] bf16 of each stream
 constexpr int SO_B = SO_XP + 4 * SB_TILE;    // gXp, gy -> gX, gF
 constexpr int SO_C = SO_B + 2 * SB_SET;      // codes
 constexpr int SO_BARS = SO_C + 2 * SB_CODES;
@@ -393,10 +384,11 @@ static_assert(SB_SMEM <= 232448, "shared memory budget");
 static_assert(SB_PHM % 1024 == 0 && W_HM % 1024 == 0 && SO_PLO % 1024 == 0 && SB_PLO % 512 == 0 &&
                   SB_TILE % 512 == 0 && SB_CODE % 256 == 0 && SO_XP % 512 == 0 && SO_C % 256 == 0,
               "tile alignment");
-// D reads 128 rows of an A tile of at most 112: what lies behind it is other data of this block
+// D reads 128 rows of an A tile of at most 96: what lies behind it is other data of this block
 static_assert(SO_PLO + SB_PLO + 128 * 64 <= SO_BARS, "operand rows");
-constexpr int SB_CONS = 8;
+constexpr int SB_CONS = 6;
 constexpr int SB_THREADS = (2 + SB_CONS) * 32;
+constexpr int SB_LOADER = 3, SB_ISSUER = 7;
 constexpr uint32_t SB_TMEM = 512;            // D twice 128 columns, gW twice 96 from column 256
 
 struct SbParams {
@@ -409,6 +401,7 @@ struct SbParams {
   const uint8_t* Fs;
   const uint8_t* wT;
   float* part_w;       // [ranges][24][4 d]
+  float* part_gain;    // [ranges][3][d]
   float* part_t;       // [d / 64][N][20]: gu, gC (as gcomb_prev is laid out)
   unsigned* status;
   int N;
@@ -480,7 +473,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     mbar_init(gwfree, SB_CONS);
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == SB_ISSUER) {
     tmem_alloc(tmem_slot, SB_TMEM);
     tmem_relinquish();
   }
@@ -489,7 +482,22 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
+  // gW of an item: accumulator s holds (stream q, column 32 s + lane of the block) in TMEM lane 32 q + lane, mix
+  // row o's three plane sums in columns o, 32 + o, 64 + o. A warp reads its own lane quarter.
+  auto gw_out = [&](int item, int s) {
+    const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256u + 96u * static_cast<uint32_t>(s);
+    uint32_t a[32], b[32], l[32];
+    tmem_ld_x32(acc, a);
+    tmem_ld_x32(acc + 32, b);
+    tmem_ld_x32(acc + 64, l);
+    float* pw = P.part_w + static_cast<size_t>(item / nblocks) * MIXN * 4 * P.d + static_cast<size_t>(warp & 3) * P.d +
+                item % nblocks * SB_COLS + 32 * s + lane;
+#pragma unroll
+    for (int o = 0; o < MIXN; ++o)
+      pw[static_cast<size_t>(o) * 4 * P.d] = __uint_as_float(a[o]) + (__uint_as_float(b[o]) + __uint_as_float(l[o]));
+  };
+
+  if (warp == SB_LOADER) {
     if (lane == 0) {
       // ---------------------------------------------------------------- loads
       const uint64_t pol = policy_evict_first();
@@ -542,8 +550,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       }
       bulk_wait<0>();
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
+  } else if (warp == SB_ISSUER) {
+    {
       // ---------------------------------------------------------------- MMAs
       constexpr uint32_t id_d = idesc_bf16_f32(128, 128);
       constexpr uint32_t id_hm = idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16);   // both MN-major
@@ -606,10 +614,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       Place cur{static_cast<int>(blockIdx.x), 0, 0, 0, 0};
       if (cur.item < items) {
         cur.tile = first_tile(cur.item);
-        product(cur, 0);
+        if (lane == 0) product(cur, 0);
       }
-      for (int u = 0; cur.item < items; ++u) {
-        const Place nx = next(cur);
+      // lane 0 issues; the warp together takes the gW rows of its lane quarter at an item's end
+      auto issue = [&](const Place& nx, int u) {
         if (nx.item < items) product(nx, u + 1);
         // gW += X'^T (r g_m) of slot u
         wait(xready, u);
@@ -629,26 +637,37 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         umma_commit(xfree);
         if (cur.s == 1) umma_commit(&pempty[pb]);
         if (cur.s == 1 && cur.tile == last_tile(cur.item) - 1) umma_commit(gwfull);
+      };
+      for (int u = 0; cur.item < items; ++u) {
+        const Place nx = next(cur);
+        if (lane == 0) issue(nx, u);
+        if (cur.s == 1 && cur.tile == last_tile(cur.item) - 1) {
+          __syncwarp();
+          wait(gwfull, cur.in);
+          tc_fence_after();
+          gw_out(cur.item, 0);
+          gw_out(cur.item, 1);
+          tc_fence_before();
+          __syncwarp();
+        }
         cur = nx;
       }
     }
   } else {
     // ------------------------------------------------------------------ consumers
     const int sub = warp & 3;            // TMEM lane quarter
-    const int h = (warp - 2) >> 2;       // which 16 columns of the slot
+    const int h = warp >> 2;             // which 16 columns of the slot
     const int tl = sub * 32 + lane;      // token row of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
-    // Threads past the tiles' height read the first row and write nothing.
-    const bool inrows = tl < SBR;
-    const int tr = inrows ? tl : 0;
-    auto row_off = [&](int q) { return tile_chunk_offset(tr, 2 * h + q); };
-    const uint32_t code_off = swizzled_chunk_offset(tr, h, 32);
+    auto row_off = [&](int q) { return tile_chunk_offset(tl, 2 * h + q); };
+    const uint32_t code_off = swizzled_chunk_offset(tl, h, 32);
     const f2 nz{P.neg_zero, P.neg_zero};
     const int nb = P.d / MX_BLOCK;
     int u = 0, in = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x, ++in) {
       const int cb = item % nblocks;
       const int tile_end = last_tile(item);
+      float gain_sum[4] = {0.f, 0.f, 0.f, 0.f};   // [slot][q], over the range's tokens of this quarter
       for (int tile = first_tile(item); tile < tile_end; ++tile) {
         const int token = tile * tt + tl;
         const bool valid = tl < tt && token < P.N;
@@ -684,12 +703,12 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           tau2 = f2{-rv.z, -rv.z};
           c12 = f2{-rv.w, -rv.w};
         }
-        float acc_u[4], acc_c[4][4];
+        f2 sum_u[4], sum_c[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          acc_u[k] = 0.f;
+          sum_u[k] = f2{0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc_c[j][k] = 0.f;
+          for (int j = 0; j < 4; ++j) sum_c[j][k] = f2{0.f, 0.f};
         }
 #pragma unroll 1
         for (int s = 0; s < 2; ++s, ++u) {
@@ -711,6 +730,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) xc[k] = *reinterpret_cast<const uint2*>(codes + k * SB_CODE + code_off + 8 * q);
             const uint2 fc = *reinterpret_cast<const uint2*>(codes + 4 * SB_CODE + code_off + 8 * q);
+            float gsum[8];   // ggain's terms of this token
             // gXp and gy, then gX and gF in their place
             uint32_t ga[4][4], ya[4], xw[4][4];
 #pragma unroll
@@ -747,7 +767,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                   xp[k] = bf2_to_f2(xw[k][w]);
                 }
                 const f2 yh = bf2_to_f2(f2_to_bf2(hc_pre_pair(cpp, xp, nz)));
-                const f2 gyh = fma2(mul2(r_y2, gn[i]), bf2_to_f2(ya[w]), mul2(tau2, yh));
+                const f2 ryg = mul2(r_y2, bf2_to_f2(ya[w]));
+                const f2 gyh = fma2(ryg, gn[i], mul2(tau2, yh));
+                const f2 gv = mul2(ryg, yh);
+                gsum[2 * w] = valid ? gv.x : 0.f;
+                gsum[2 * w + 1] = valid ? gv.y : 0.f;
                 f2 G[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -755,10 +779,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                   f2 v = fma2(cpp[k], gyh, bf2_to_f2(ga[k][w]));
                   v = add2(v, gmix);
                   G[k] = fma2(c12, xp[k], v);
-                  acc_u[k] = fmaf(G[k].x, f.x, fmaf(G[k].y, f.y, acc_u[k]));
+                  sum_u[k] = fma2(G[k], f, sum_u[k]);
 #pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    acc_c[j][k] = fmaf(G[k].x, x[j].x, fmaf(G[k].y, x[j].y, acc_c[j][k]));
+                  for (int j = 0; j < 4; ++j) sum_c[j][k] = fma2(G[k], x[j], sum_c[j][k]);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -775,7 +798,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 ya[w] = f2_to_bf2(vf);
               }
             }
-            if (inrows) {
+            {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 *reinterpret_cast<uint4*>(sm + SO_XP + k * SB_TILE + row_off(q)) =
@@ -784,6 +807,14 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                     make_uint4(ga[k][0], ga[k][1], ga[k][2], ga[k][3]);
               }
               *reinterpret_cast<uint4*>(bt + 4 * SB_TILE + row_off(q)) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
+            }
+            const float gt = warp_sums<8>(gsum);   // lane l: column l % 8
+            if (s == 0) {
+              if (q == 0) gain_sum[0] += gt;
+              else gain_sum[1] += gt;
+            } else {
+              if (q == 0) gain_sum[2] += gt;
+              else gain_sum[3] += gt;
             }
           }
           tc_fence_before();   // the TMEM loads above, before the MMA that reuses the buffer
@@ -800,9 +831,16 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         // which both threads have read
         {
           const int e = (u - 1) & 1;
-          uint8_t* codes = sm + SO_C + e * SB_CODES + swizzled_chunk_offset(tr, 0, 32);
+          uint8_t* codes = sm + SO_C + e * SB_CODES + swizzled_chunk_offset(tl, 0, 32);
+          float acc_u[4], acc_c[4][4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc_u[k] = sum_u[k].x + sum_u[k].y;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc_c[j][k] = sum_c[j][k].x + sum_c[j][k].y;
+          }
           named_bar_sync(1 + sub, 64);
-          if (h == 1 && inrows) {
+          if (h == 1) {
             *reinterpret_cast<float4*>(codes) = make_float4(acc_u[0], acc_u[1], acc_u[2], acc_u[3]);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -833,23 +871,16 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           if (lane == 0) mbar_arrive(&cempty[e]);
         }
       }
-      // gW of the item: accumulator h holds (stream sub, column 32 h + lane of the block) in this lane's row,
-      // mix row o's three plane sums in columns o, 32 + o, 64 + o
+      if (lane < 8) {
+        float* pg = P.part_gain + (static_cast<size_t>(item / nblocks) * 3 + sub) * P.d + cb * SB_COLS + 16 * h + lane;
+        pg[0] = gain_sum[0];
+        pg[8] = gain_sum[1];
+        pg[32] = gain_sum[2];
+        pg[40] = gain_sum[3];
+      }
       wait(gwfull, in);
       tc_fence_after();
-      {
-        const uint32_t acc = lane_base + 256u + 96u * static_cast<uint32_t>(h);
-        uint32_t a[32], b[32], l[32];
-        tmem_ld_x32(acc, a);
-        tmem_ld_x32(acc + 32, b);
-        tmem_ld_x32(acc + 64, l);
-        float* pw = P.part_w + static_cast<size_t>(item / nblocks) * MIXN * 4 * P.d +
-                    static_cast<size_t>(sub) * P.d + cb * SB_COLS + 32 * h + lane;
-#pragma unroll
-        for (int o = 0; o < MIXN; ++o)
-          pw[static_cast<size_t>(o) * 4 * P.d] =
-              __uint_as_float(a[o]) + (__uint_as_float(b[o]) + __uint_as_float(l[o]));
-      }
+      gw_out(item, h);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(gwfree);
@@ -859,12 +890,12 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   if (timed_out) atomicOr(P.status, STATUS_TIMEOUT);
   tc_fence_before();
   block_sync();
-  if (warp == 1) tmem_dealloc(tmem, SB_TMEM);
+  if (warp == SB_ISSUER) tmem_dealloc(tmem, SB_TMEM);
 }
 
 // ---------------------------------------------------------------------------------------------
 // ckb_reduce_kernel: float4 sums of partials in their order. Blocks [0, gw) sum gW over the ranges,
-// [gw, gw + gg) ggain over the token kernel's blocks (8 threads an output), [.., + gt) gu and gC of the tokens
+// [gw, gw + gg) ggain over the ranges and lane quarters (8 threads an output), [.., + gt) gu and gC of the tokens
 // over the column blocks, and the last one g_base and g_scale.
 struct ReduceParams {
   const float* part_w;
@@ -948,7 +979,7 @@ __global__ void __launch_bounds__(256) ckb_reduce_kernel(const ReduceParams P) {
 struct Plan {
   size_t wt, gm, rec, hm, lo, mix, gain, w, t, bytes;
   int tt, ntiles, per, ranges;   // stream kernel
-  int mix_blocks, gain_rows;
+  int mix_blocks;
 };
 
 // Token tiles of tt rows in `ranges` ranges of `per` tiles: the busiest block's items x tiles x time of a
@@ -978,7 +1009,6 @@ Plan plan_of(int64_t N, int d, int sms) {
     }
   }
   p.mix_blocks = static_cast<int>((N + PREP_TOKENS - 1) / PREP_TOKENS);
-  p.gain_rows = static_cast<int>(std::min<int64_t>(std::max<int64_t>(N, 1), 2 * static_cast<int64_t>(sms)));
   size_t off = 0;
   auto part = [&](size_t bytes) {
     const size_t at = off;
@@ -992,7 +1022,7 @@ Plan plan_of(int64_t N, int d, int sms) {
   p.hm = part(n * 128);
   p.lo = part(n * 64);
   p.mix = part(static_cast<size_t>(p.mix_blocks) * 128);
-  p.gain = part(static_cast<size_t>(p.gain_rows) * d * 4);
+  p.gain = part(static_cast<size_t>(p.ranges) * 3 * d * 4);
   p.w = part(static_cast<size_t>(p.ranges) * MIXN * 4 * d * 4);
   p.t = part(static_cast<size_t>(nblocks) * n * 80);
   p.bytes = off;
@@ -1044,19 +1074,16 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
   {
     const CkIn in{static_cast<const uint2*>(ck.X_codes), static_cast<const uint8_t*>(ck.X_scale),
                   static_cast<const uint2*>(ck.F_codes), static_cast<const uint8_t*>(ck.F_scale)};
-    auto run = [&](auto kernel, int ch) {
-      const int threads = ((d / 8 + ch - 1) / ch + 31) / 32 * 32;
-      kernel<<<p.gain_rows, threads, 0, stream>>>(
+    auto run = [&](auto kernel, int64_t blocks) {
+      kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 2 * static_cast<int64_t>(sms))), TOKEN_WARPS * 32, 0, stream>>>(
           in, static_cast<const uint4*>(a.gy), a.pre_prev, a.post_prev, a.comb_prev, a.gain, a.mixes, wsf(p.gm),
           wsf(p.rec), reinterpret_cast<__nv_bfloat16*>(ws + p.hm), reinterpret_cast<__nv_bfloat16*>(ws + p.lo),
-          a.gpre_prev, wsf(p.gain), N, d, a.norm_eps, row_dest, -0.0f);
+          a.gpre_prev, N, d, a.norm_eps, row_dest, -0.0f);
       return cudaGetLastError();
     };
-    const int chunks = d / 8, most = TOKEN_WARPS * 32;
-    e = chunks <= most ? run(ckb_token_kernel<1>, 1)
-        : chunks <= 2 * most ? run(ckb_token_kernel<2>, 2)
-        : chunks <= 4 * most ? run(ckb_token_kernel<4>, 4)
-                             : run(ckb_token_kernel<8>, 8);
+    // a warp a token once every warp the device holds (two blocks a multiprocessor) has one
+    e = N >= 2 * static_cast<int64_t>(sms) * TOKEN_WARPS ? run(ckb_token_kernel<1>, (N + TOKEN_WARPS - 1) / TOKEN_WARPS)
+                                                         : run(ckb_token_kernel<TOKEN_WARPS>, N);
     if (e != cudaSuccess) return e;
   }
   {
@@ -1078,6 +1105,7 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
     P.Fs = static_cast<const uint8_t*>(ck.F_scale);
     P.wT = ws + p.wt;
     P.part_w = wsf(p.w);
+    P.part_gain = wsf(p.gain);
     P.part_t = wsf(p.t);
     P.status = status;
     P.N = static_cast<int>(N);
@@ -1109,7 +1137,7 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
   R.N = N;
   R.d = d;
   R.ranges = p.ranges;
-  R.gain_rows = p.gain_rows;
+  R.gain_rows = 3 * p.ranges;
   R.mix_blocks = p.mix_blocks;
   R.gw = (MIXN * d + 255) / 256;
   R.gg = (d / 4 + 31) / 32;

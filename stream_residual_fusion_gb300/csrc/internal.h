@@ -175,9 +175,8 @@ struct BwdCheckpoint {
   const void* F_codes;    // uint8 [N, d]
   const void* F_scale;    // uint8 [N, d / 32]
 };
-// Its workspace; 0 where bwd_layout's is and for d over kCkptMaxWidth.
+// Its workspace; 0 like bwd_layout.
 size_t bwd_ckpt_bytes(int64_t N, int d);
-constexpr int kCkptMaxWidth = 24576;   // 8 chunks of 8 features for each of 384 threads
 cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& c, cudaStream_t stream);
 
 // Activation checkpoints (checkpoint.cu): bf16 rows of d features to MXFP8 and back.
