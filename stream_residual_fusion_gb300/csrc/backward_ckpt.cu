@@ -8,17 +8,16 @@
 //   ckb_prep_kernel    the split's and Sinkhorn's derivatives (g_m), four lanes a token, one row of the
 //                      4 x 4 matrix each; beside them, in blocks of their own, the bf16 planes of W^T.
 //   ckb_token_kernel   one warp or one block a token: the sums over its width that give r, r_y, tau, c1 and gp, the
-//                      three bf16 planes of r g_m.
-//   ckb_stream_kernel  work items of (64 columns of every stream, a range of token tiles): gX, gF, ggain and
-//                      gW, for which X' never leaves the SM (below).
+//                      three bf16 planes of r g_m; and the scale codes once more, slot by slot.
+//   ckb_stream_kernel  work items of (up to 256 columns of every stream, a range of token tiles): gX, gF, ggain
+//                      and gW, for which X' never leaves the SM (below).
 //   ckb_reduce_kernel  sums of partials in a fixed order: gW, ggain, g_base, g_scale, and gu, gC of every
 //                      token over the column blocks.
 //
-// Why the stream kernel owns columns and walks tokens: W^T of its columns stays in shared memory, the
-// gW accumulators stay in TMEM over the range, X' feeds its tensor-core product from shared memory
-// right after it was formed (backward.cu reads X' and gy a second time for that), and a few tokens
-// already give every SM work: d / 64 items a tile. The price is gu and gC in d / 64 parts, 1.25 d bytes a
-// token written and read again.
+// Why the stream kernel owns columns and walks tokens: the gW accumulators of its columns stay in TMEM over
+// the range, X' feeds their tensor-core product from shared memory right after it was formed (backward.cu
+// reads X' and gy a second time for that), and a few tokens already give many SMs work. The price is gu
+// and gC in as many parts as there are column blocks, 80 bytes a token and block written and read again.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -58,7 +57,6 @@ constexpr int PREP_TOKENS = PREP_THREADS / 4;
 // Sinkhorn step inputs kept a token (shared memory, 64 bytes each): all of them up to 24 rounds, every
 // second one up to 48, ...
 constexpr int PREP_KEEP = 47;
-constexpr int SB_COLS = 64;                      // columns of a work item of the stream kernel
 constexpr int W_HM = 128 * 128;                  // W^T hi and mid planes of 32 columns: 128 rows x 128 bytes
 constexpr int W_LO = 128 * 64;                   // lo plane
 constexpr int W_SLOT = W_HM + W_LO;
@@ -231,7 +229,8 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
     const CkIn in, const uint4* __restrict__ gy, const float* __restrict__ pre, const float* __restrict__ post,
     const float* __restrict__ comb, const float* __restrict__ gain, const float* __restrict__ mixes,
     const float* __restrict__ gm, float* __restrict__ rec, __nv_bfloat16* __restrict__ planes_hm,
-    __nv_bfloat16* __restrict__ planes_lo, float* __restrict__ gpre_prev, int64_t N, int d, float norm_eps,
+    __nv_bfloat16* __restrict__ planes_lo, float* __restrict__ gpre_prev, uint2* __restrict__ slot_scales,
+    int64_t scale_rows, int64_t N, int d, float norm_eps,
     int row_dest, float neg_zero) {
   constexpr int V = 16;   // |x|^2, |y_hat|^2, T, gain gy . X'_j, y_hat . X'_j
   __shared__ float scratch[2][TOKEN_WARPS * V];
@@ -298,6 +297,9 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
       float sx[5];
 #pragma unroll
       for (int k = 0; k < 5; ++k) sx[k] = scale_value(cur.s[k]);
+      if ((c & 3) == 0)   // the block's five scale codes, for the stream kernel
+        slot_scales[(c / 4) * scale_rows + t] =
+            make_uint2(cur.s[0] | (cur.s[1] << 8) | (cur.s[2] << 16) | (cur.s[3] << 24), cur.s[4]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         auto word = [&](uint2 w) { return (i < 2 ? w.x : w.y) >> (16 * (i & 1)); };
@@ -351,11 +353,11 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
 // ---------------------------------------------------------------------------------------------
 // ckb_stream_kernel: per work item, W^T (r g_m) and gW on the tensor cores around the elementwise
 // gradients. A tile is up to 96 tokens; a slot is 32 columns of every stream of a tile.
-//   warp 3, lane 0   TMA loads: codes (2 slots ahead), gXp and gy (2 slots), the tile's planes of r g_m.
+//   warp 3, lane 0   TMA loads, two slots ahead: codes, gXp and gy, W^T; and the tile's planes of r g_m.
 //   warp 3, lane 1   TMA stores of gX, gF, which were written over gXp and gy.
-//   warp 7, lane 0   W^T of the item's columns, and the MMAs: D = A W^T^T for the next slot (A = the planes
-//                    [tokens x 24] of r g_m, six products of planes, the three largest orders), then
-//                    gW += X'^T A of this slot once the consumers have laid X' down.
+//   warp 7, lane 0   the MMAs: D = A W^T^T for the next slot (A = the planes [tokens x 24] of r g_m; the six
+//                    products of planes of the three largest orders), then gW += X'^T A of this slot, its three
+//                    planes into one accumulator, once the consumers have laid X' down.
 //   the others       two threads a token, 16 columns of the slot each, and ggain of those columns.
 // Eight warps leave each thread 255 registers, which its token's weights (as pairs), sums and operands take:
 // with ten (168 registers) what was spilled missed the little L1 beside 220 KB of shared memory, and a slot
@@ -369,16 +371,21 @@ constexpr int SB_TILE = SBR * 64;            // [96 x 32] bf16
 constexpr int SB_SET = 5 * SB_TILE;
 constexpr int SB_PHM = SBR * 128;            // planes of r g_m: hi and mid
 constexpr int SB_PLO = SBR * 64;
-constexpr int SO_PHM = 0;                    // two of each, then the item's W^T (two slots)
+constexpr int SO_PHM = 0;                    // two of each, then W^T of two slots
 constexpr int SO_WHM = SO_PHM + 2 * SB_PHM;
 constexpr int SO_WLO = SO_WHM + 2 * W_HM;
 constexpr int SO_PLO = SO_WLO + 2 * W_LO;
 constexpr int SO_XP = SO_PLO + 2 * SB_PLO;   // X' of the slot, [96 x 32] bf16 of each stream
 constexpr int SO_B = SO_XP + 4 * SB_TILE;    // gXp, gy -> gX, gF
 constexpr int SO_C = SO_B + 2 * SB_SET;      // codes
-constexpr int SO_BARS = SO_C + 2 * SB_CODES;
-constexpr int SB_NBARS = 2 * 9 + 6;
-constexpr int SO_TMEM = SO_BARS + SB_NBARS * 8;
+constexpr int SB_SCALES = SBR * 8;           // scale codes of a slot, then its 32 gains
+constexpr int SB_SIDE = SB_SCALES + 128;
+constexpr int SO_S = SO_C + 2 * SB_CODES;
+constexpr int SO_BARS = SO_S + 2 * SB_SIDE;
+constexpr int SB_NBARS = 2 * 11 + 4;
+constexpr int SB_SLOTS = 8;                  // slots of a work item, at most
+constexpr int SO_GAIN = SO_BARS + SB_NBARS * 8;   // ggain sums: [6 warps][slot][16 columns]
+constexpr int SO_TMEM = SO_GAIN + 6 * SB_SLOTS * 16 * 4;
 constexpr int SB_SMEM = SO_TMEM + 16 + 1024;
 static_assert(SB_SMEM <= 232448, "shared memory budget");
 static_assert(SB_PHM % 1024 == 0 && W_HM % 1024 == 0 && SO_PLO % 1024 == 0 && SB_PLO % 512 == 0 &&
@@ -389,7 +396,7 @@ static_assert(SO_PLO + SB_PLO + 128 * 64 <= SO_BARS, "operand rows");
 constexpr int SB_CONS = 6;
 constexpr int SB_THREADS = (2 + SB_CONS) * 32;
 constexpr int SB_LOADER = 3, SB_ISSUER = 7;
-constexpr uint32_t SB_TMEM = 512;            // D twice 128 columns, gW twice 96 from column 256
+constexpr uint32_t SB_TMEM = 512;            // D twice 128 columns, gW 32 columns a slot from column 256
 
 struct SbParams {
   const float* pre;
@@ -397,12 +404,11 @@ struct SbParams {
   const float* comb;
   const float* rec;
   const float* gain;
-  const uint8_t* Xs;
-  const uint8_t* Fs;
+  const uint2* scales; // [d / 32][ntiles tt]: codes of X's four rows (low byte first) and of F's
   const uint8_t* wT;
   float* part_w;       // [ranges][24][4 d]
   float* part_gain;    // [ranges][3][d]
-  float* part_t;       // [d / 64][N][20]: gu, gC (as gcomb_prev is laid out)
+  float* part_t;       // [column blocks][N][20]: gu, gC (as gcomb_prev is laid out)
   unsigned* status;
   int N;
   int d;
@@ -410,6 +416,8 @@ struct SbParams {
   int ntiles;
   int per;             // tiles of a range
   int ranges;
+  int spb;             // slots of a column block
+  int nblocks;         // column blocks
   float neg_zero;
   int row_dest;
 };
@@ -433,8 +441,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   uint64_t* pfull = dfree + 2;
   uint64_t* pempty = pfull + 2;
   uint64_t* wfull = pempty + 2;
-  uint64_t* wempty = wfull + 1;
-  uint64_t* xready = wempty + 1;
+  uint64_t* wempty = wfull + 2;
+  uint64_t* xready = wempty + 2;
   uint64_t* xfree = xready + 1;
   uint64_t* gwfull = xfree + 1;
   uint64_t* gwfree = gwfull + 1;
@@ -442,7 +450,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tt = P.tt;
-  const int nblocks = P.d / SB_COLS;
+  const int nblocks = P.nblocks;
   const int items = nblocks * P.ranges;
   bool timed_out = false;
   auto limit = [&]() { return timed_out ? 0ull : BWD_WAIT_NS; };
@@ -452,6 +460,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   // the tiles of an item
   auto first_tile = [&](int item) { return item / nblocks * P.per; };
   auto last_tile = [&](int item) { return min(P.ntiles, first_tile(item) + P.per); };
+  // its first column and its slots
+  auto column = [&](int item) { return item % nblocks * P.spb * 32; };
+  auto slots = [&](int item) { return min(P.spb, P.d / 32 - item % nblocks * P.spb); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -464,9 +475,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       mbar_init(&dfree[i], SB_CONS);
       mbar_init(&pfull[i], 1);
       mbar_init(&pempty[i], 1);
+      mbar_init(&wfull[i], 1);
+      mbar_init(&wempty[i], 1);
     }
-    mbar_init(wfull, 1);
-    mbar_init(wempty, 1);
     mbar_init(xready, SB_CONS);
     mbar_init(xfree, 1);
     mbar_init(gwfull, 1);
@@ -483,42 +494,46 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   const uint32_t tmem = *tmem_slot;
 
   // gW of an item: accumulator s holds (stream q, column 32 s + lane of the block) in TMEM lane 32 q + lane, mix
-  // row o's three plane sums in columns o, 32 + o, 64 + o. A warp reads its own lane quarter.
+  // row o in column o. A warp reads its own lane quarter.
   auto gw_out = [&](int item, int s) {
-    const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256u + 96u * static_cast<uint32_t>(s);
-    uint32_t a[32], b[32], l[32];
-    tmem_ld_x32(acc, a);
-    tmem_ld_x32(acc + 32, b);
-    tmem_ld_x32(acc + 64, l);
+    uint32_t a[32];
+    tmem_ld_x32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256u + 32u * static_cast<uint32_t>(s), a);
     float* pw = P.part_w + static_cast<size_t>(item / nblocks) * MIXN * 4 * P.d + static_cast<size_t>(warp & 3) * P.d +
-                item % nblocks * SB_COLS + 32 * s + lane;
+                column(item) + 32 * s + lane;
 #pragma unroll
-    for (int o = 0; o < MIXN; ++o)
-      pw[static_cast<size_t>(o) * 4 * P.d] = __uint_as_float(a[o]) + (__uint_as_float(b[o]) + __uint_as_float(l[o]));
+    for (int o = 0; o < MIXN; ++o) pw[static_cast<size_t>(o) * 4 * P.d] = __uint_as_float(a[o]);
   };
 
   if (warp == SB_LOADER) {
     if (lane == 0) {
       // ---------------------------------------------------------------- loads
-      const uint64_t pol = policy_evict_first();
-      const uint32_t code_bytes = 5u * 32u * tt, b_bytes = 5u * 64u * tt;
+      const uint64_t pol = policy_evict_normal(), wpol = policy_evict_last();
+      const uint32_t code_bytes = (5u * 32u + 8u) * tt + 128u, b_bytes = 5u * 64u * tt;
       int u = 0, tn = 0;   // slots and tiles of this block so far
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int cb = item % nblocks;
+        const int col0 = column(item), ns = slots(item);
         for (int tile = first_tile(item); tile < last_tile(item); ++tile, ++tn) {
           const int t0 = tile * tt, pb = tn & 1;
           if (tn >= 2) wait(&pempty[pb], (tn >> 1) - 1);
           mbar_arrive_expect_tx(&pfull[pb], static_cast<uint32_t>(192 * tt));
           tma_load_2d(sm + SO_PHM + pb * SB_PHM, &tm_hm, &pfull[pb], 0, t0);
           tma_load_2d(sm + SO_PLO + pb * SB_PLO, &tm_lo, &pfull[pb], 0, t0);
-          for (int s = 0; s < 2; ++s, ++u) {
-            const int e = u & 1, col = cb * SB_COLS + 32 * s;
+          for (int s = 0; s < ns; ++s, ++u) {
+            const int e = u & 1, col = col0 + 32 * s;
+            if (u >= 2) wait(&wempty[e], (u >> 1) - 1);
+            mbar_arrive_expect_tx(&wfull[e], static_cast<uint32_t>(W_SLOT));
+            const uint8_t* w = P.wT + static_cast<size_t>(col / 32) * W_SLOT;
+            bulk_load_hint(sm + SO_WHM + e * W_HM, w, W_HM, &wfull[e], wpol);
+            bulk_load_hint(sm + SO_WLO + e * W_LO, w + W_HM, W_LO, &wfull[e], wpol);
             if (u >= 2) wait(&cempty[e], (u >> 1) - 1);
             mbar_arrive_expect_tx(&cfull[e], code_bytes);
             uint8_t* c = sm + SO_C + e * SB_CODES;
 #pragma unroll
             for (int k = 0; k < 4; ++k) tma_load_3d_hint(c + k * SB_CODE, &tm_x, &cfull[e], col, k, t0, pol);
             tma_load_2d_hint(c + 4 * SB_CODE, &tm_f, &cfull[e], col, t0, pol);
+            uint8_t* side = sm + SO_S + e * SB_SIDE;
+            bulk_load_hint(side, P.scales + (static_cast<size_t>(col / 32) * P.ntiles * tt + t0), 8u * tt, &cfull[e], pol);
+            bulk_load_hint(side + SB_SCALES, P.gain + col, 128, &cfull[e], wpol);
             if (u >= 2) wait(&bempty[e], (u >> 1) - 1);
             mbar_arrive_expect_tx(&bfull[e], b_bytes);
             uint8_t* b = sm + SO_B + e * SB_SET;
@@ -533,10 +548,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       const uint64_t pol = policy_evict_first();
       int u = 0;
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int cb = item % nblocks;
+        const int col0 = column(item), ns = slots(item);
         for (int tile = first_tile(item); tile < last_tile(item); ++tile) {
-          for (int s = 0; s < 2; ++s, ++u) {
-            const int e = u & 1, col = cb * SB_COLS + 32 * s, t0 = tile * tt;
+          for (int s = 0; s < ns; ++s, ++u) {
+            const int e = u & 1, col = col0 + 32 * s, t0 = tile * tt;
             wait(&gready[e], u >> 1);
             const uint8_t* b = sm + SO_B + e * SB_SET;
 #pragma unroll
@@ -554,18 +569,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     {
       // ---------------------------------------------------------------- MMAs
       constexpr uint32_t id_d = idesc_bf16_f32(128, 128);
-      constexpr uint32_t id_hm = idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16);   // both MN-major
-      constexpr uint32_t id_lo = idesc_bf16_f32(128, 32) | (1u << 15) | (1u << 16);
-      const uint64_t wpol = policy_evict_last();
-      // where the product of slot u (u the slot's number in this block) is: its item, tile and half
+      constexpr uint32_t id_w = idesc_bf16_f32(128, 32) | (1u << 15) | (1u << 16);   // both MN-major
+      // where slot u (u the slot's number in this block) is: its item, tile and place in the tile
       struct Place {
         int item, tile, s, tn, in;   // in: items before it
       };
       auto next = [&](Place p) {
-        if (p.s == 0) {
-          p.s = 1;
-          return p;
-        }
+        if (++p.s < slots(p.item)) return p;
         p.s = 0;
         ++p.tn;
         if (++p.tile >= last_tile(p.item)) {
@@ -576,22 +586,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         return p;
       };
       auto product = [&](const Place& p, int u) {   // D of slot u
-        if (p.s == 0 && p.tile == first_tile(p.item)) {
-          if (p.in > 0) wait(wempty, p.in - 1);
-          mbar_arrive_expect_tx(wfull, 2u * W_SLOT);
-          const uint8_t* w = P.wT + static_cast<size_t>(p.item % nblocks) * 2 * W_SLOT;
-          for (int s = 0; s < 2; ++s) {
-            bulk_load_hint(sm + SO_WHM + s * W_HM, w + s * W_SLOT, W_HM, wfull, wpol);
-            bulk_load_hint(sm + SO_WLO + s * W_LO, w + s * W_SLOT + W_HM, W_LO, wfull, wpol);
-          }
-          wait(wfull, p.in);
-        }
         const int pb = p.tn & 1, db = u & 1;
         if (p.s == 0) wait(&pfull[pb], p.tn >> 1);
+        wait(&wfull[db], u >> 1);
         if (u >= 2) wait(&dfree[db], (u >> 1) - 1);
         tc_fence_after();
         const uint32_t ahm = smem_u32(sm + SO_PHM + pb * SB_PHM), alo = smem_u32(sm + SO_PLO + pb * SB_PLO);
-        const uint32_t bhm = smem_u32(sm + SO_WHM + p.s * W_HM), blo = smem_u32(sm + SO_WLO + p.s * W_LO);
+        const uint32_t bhm = smem_u32(sm + SO_WHM + db * W_HM), blo = smem_u32(sm + SO_WLO + db * W_LO);
         auto a_of = [&](int pl, int kk) {
           return pl == 2 ? sdesc_kmajor_swizzled(alo + 32 * kk, 64) : sdesc_kmajor_swizzled(ahm + 64 * pl + 32 * kk, 128);
         };
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
               more = 1;
             }
         umma_commit(&dready[db]);
-        if (p.s == 1 && p.tile == last_tile(p.item) - 1) umma_commit(wempty);
+        umma_commit(&wempty[db]);
       };
       Place cur{static_cast<int>(blockIdx.x), 0, 0, 0, 0};
       if (cur.item < items) {
@@ -627,26 +628,26 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         const int pb = cur.tn & 1;
         const uint32_t xa = smem_u32(sm + SO_XP);
         const uint32_t phm = smem_u32(sm + SO_PHM + pb * SB_PHM), plo = smem_u32(sm + SO_PLO + pb * SB_PLO);
-        const uint32_t acc = tmem + 256u + 96u * static_cast<uint32_t>(cur.s);
+        const uint32_t acc = tmem + 256u + 32u * static_cast<uint32_t>(cur.s);
+        const bool last = cur.s == slots(cur.item) - 1;
         for (int ks = 0; ks < tt / 16; ++ks) {
           const uint64_t a = sdesc_mnmajor(xa + ks * 1024, 64, SB_TILE, 512);
-          const uint32_t more = (start && ks == 0) ? 0u : 1u;
-          umma_bf16(acc, a, sdesc_mnmajor(phm + ks * 2048, 128, 0, 1024), id_hm, more);
-          umma_bf16(acc + 64, a, sdesc_mnmajor(plo + ks * 1024, 64, 0, 512), id_lo, more);
+          umma_bf16(acc, a, sdesc_mnmajor(plo + ks * 1024, 64, 0, 512), id_w, (start && ks == 0) ? 0u : 1u);
+          umma_bf16(acc, a, sdesc_mnmajor(phm + 64 + ks * 2048, 128, 0, 1024), id_w, 1u);
+          umma_bf16(acc, a, sdesc_mnmajor(phm + ks * 2048, 128, 0, 1024), id_w, 1u);
         }
         umma_commit(xfree);
-        if (cur.s == 1) umma_commit(&pempty[pb]);
-        if (cur.s == 1 && cur.tile == last_tile(cur.item) - 1) umma_commit(gwfull);
+        if (last) umma_commit(&pempty[pb]);
+        if (last && cur.tile == last_tile(cur.item) - 1) umma_commit(gwfull);
       };
       for (int u = 0; cur.item < items; ++u) {
         const Place nx = next(cur);
         if (lane == 0) issue(nx, u);
-        if (cur.s == 1 && cur.tile == last_tile(cur.item) - 1) {
+        if (cur.s == slots(cur.item) - 1 && cur.tile == last_tile(cur.item) - 1) {
           __syncwarp();
           wait(gwfull, cur.in);
           tc_fence_after();
-          gw_out(cur.item, 0);
-          gw_out(cur.item, 1);
+          for (int q = 0; q < slots(cur.item); ++q) gw_out(cur.item, q);
           tc_fence_before();
           __syncwarp();
         }
@@ -662,12 +663,15 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     auto row_off = [&](int q) { return tile_chunk_offset(tl, 2 * h + q); };
     const uint32_t code_off = swizzled_chunk_offset(tl, h, 32);
     const f2 nz{P.neg_zero, P.neg_zero};
-    const int nb = P.d / MX_BLOCK;
     int u = 0, in = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x, ++in) {
-      const int cb = item % nblocks;
+      const int cb = item % nblocks, col0 = column(item), ns = slots(item);
       const int tile_end = last_tile(item);
-      float gain_sum[4] = {0.f, 0.f, 0.f, 0.f};   // [slot][q], over the range's tokens of this quarter
+      // this warp's sums of ggain over the range's tokens of its quarter: lane l has columns l and l + 8 of its
+      // 16 in each slot
+      float* gain_sum = reinterpret_cast<float*>(sm + SO_GAIN) + (sub + 3 * h) * SB_SLOTS * 16 + (lane & 7);
+      if (lane < 8)
+        for (int s = 0; s < 2 * ns; ++s) gain_sum[8 * s] = 0.f;
       for (int tile = first_tile(item); tile < tile_end; ++tile) {
         const int token = tile * tt + tl;
         const bool valid = tl < tt && token < P.N;
@@ -675,17 +679,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         // cc[j][k] = weight of input stream j in output stream k
         f2 cc[4][4], cu[4], cpp[4];
         f2 r_y2, tau2, c12;
-        uint32_t xs[4], fs;   // this item's two scale codes of each row
         {
           const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-          auto ld = [&](const float* p, size_t i) { return valid ? __ldg(reinterpret_cast<const float4*>(p) + i) : zero; };
+          // read once: not to push what spills out of the small L1
+          auto ld = [&](const float* p, size_t i) { return valid ? __ldcs(reinterpret_cast<const float4*>(p) + i) : zero; };
           const float4 c0 = ld(P.comb, row * 4), c1 = ld(P.comb, row * 4 + 1), c2 = ld(P.comb, row * 4 + 2),
                        c3 = ld(P.comb, row * 4 + 3);
           const float4 uv = ld(P.post, row), pv = ld(P.pre, row), rv = ld(P.rec, row);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            xs[k] = valid ? __ldg(reinterpret_cast<const uint16_t*>(P.Xs + (row * 4 + k) * nb) + cb) : 0u;
-          fs = valid ? __ldg(reinterpret_cast<const uint16_t*>(P.Fs + row * nb) + cb) : 0u;
           const float cm[16] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w,
                                 c2.x, c2.y, c2.z, c2.w, c3.x, c3.y, c3.z, c3.w};
           const float uu[4] = {uv.x, uv.y, uv.z, uv.w}, pp[4] = {pv.x, pv.y, pv.z, pv.w};
@@ -711,19 +711,23 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           for (int j = 0; j < 4; ++j) sum_c[j][k] = f2{0.f, 0.f};
         }
 #pragma unroll 1
-        for (int s = 0; s < 2; ++s, ++u) {
+        for (int s = 0; s < ns; ++s, ++u) {
           const int e = u & 1;
           uint8_t* codes = sm + SO_C + e * SB_CODES;
           uint8_t* bt = sm + SO_B + e * SB_SET;
           wait(&cfull[e], u >> 1);
           wait(&bfull[e], u >> 1);
           wait(&dready[e], u >> 1);
-          if (u > 0) wait(xfree, u - 1);
           tc_fence_after();
-          float sx[4];
+          const uint8_t* side = sm + SO_S + e * SB_SIDE;
+          float sx[4], sf;
+          {
+            uint2 v = *reinterpret_cast<const uint2*>(side + 8 * tl);
+            if (!valid) v = make_uint2(0u, 0u);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sx[k] = scale_value((xs[k] >> (8 * s)) & 0xffu);
-          const float sf = scale_value((fs >> (8 * s)) & 0xffu);
+            for (int k = 0; k < 4; ++k) sx[k] = scale_value((v.x >> (8 * k)) & 0xffu);
+            sf = scale_value(v.y);
+          }
 #pragma unroll 1
           for (int q = 0; q < 2; ++q) {
             uint2 xc[4];
@@ -749,7 +753,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 tmem_ld_x4_nowait(lane_base + static_cast<uint32_t>(e * 128 + k * 32 + 16 * h + 8 * q + 4 * hq), gw[k]);
-              const float4 g0 = __ldg(reinterpret_cast<const float4*>(P.gain + cb * SB_COLS + 32 * s + 16 * h + 8 * q + 4 * hq));
+              const float4 g0 = *reinterpret_cast<const float4*>(side + SB_SCALES + 4 * (16 * h + 8 * q + 4 * hq));
               const f2 gn[2] = {f2{g0.x, g0.y}, f2{g0.z, g0.w}};
               tmem_ld_wait();
 #pragma unroll
@@ -798,6 +802,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 ya[w] = f2_to_bf2(vf);
               }
             }
+            if (q == 0 && u > 0) wait(xfree, u - 1);   // gW has read the last slot's X'
             {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -809,13 +814,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
               *reinterpret_cast<uint4*>(bt + 4 * SB_TILE + row_off(q)) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
             }
             const float gt = warp_sums<8>(gsum);   // lane l: column l % 8
-            if (s == 0) {
-              if (q == 0) gain_sum[0] += gt;
-              else gain_sum[1] += gt;
-            } else {
-              if (q == 0) gain_sum[2] += gt;
-              else gain_sum[3] += gt;
-            }
+            if (lane < 8) gain_sum[16 * s + 8 * q] += gt;
           }
           tc_fence_before();   // the TMEM loads above, before the MMA that reuses the buffer
           fence_proxy_async_smem();
@@ -824,7 +823,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             mbar_arrive(&dfree[e]);
             mbar_arrive(xready);
             mbar_arrive(&gready[e]);
-            if (s == 0) mbar_arrive(&cempty[e]);
+            if (s < ns - 1) mbar_arrive(&cempty[e]);
           }
         }
         // gu and gC of the item's columns: the second thread's sums through the codes' rows of this token,
@@ -872,15 +871,15 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         }
       }
       if (lane < 8) {
-        float* pg = P.part_gain + (static_cast<size_t>(item / nblocks) * 3 + sub) * P.d + cb * SB_COLS + 16 * h + lane;
-        pg[0] = gain_sum[0];
-        pg[8] = gain_sum[1];
-        pg[32] = gain_sum[2];
-        pg[40] = gain_sum[3];
+        float* pg = P.part_gain + (static_cast<size_t>(item / nblocks) * 3 + sub) * P.d + col0 + 16 * h + lane;
+        for (int s = 0; s < ns; ++s) {
+          pg[32 * s] = gain_sum[16 * s];
+          pg[32 * s + 8] = gain_sum[16 * s + 8];
+        }
       }
       wait(gwfull, in);
       tc_fence_after();
-      gw_out(item, h);
+      for (int s = h; s < ns; s += 2) gw_out(item, s);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(gwfree);
@@ -910,7 +909,7 @@ struct ReduceParams {
   float* gscale;
   int64_t N;
   int d;
-  int ranges, gain_rows, mix_blocks;
+  int ranges, gain_rows, mix_blocks, col_blocks;
   int gw, gg;
   int64_t gt;
 };
@@ -948,9 +947,8 @@ __global__ void __launch_bounds__(256) ckb_reduce_kernel(const ReduceParams P) {
     const int64_t n4 = P.N * 5, i = (blk - P.gw - P.gg) * 256 + threadIdx.x;
     if (i >= n4) return;
     float4 v = zero;
-    const int nblocks = P.d / SB_COLS;
 #pragma unroll 8
-    for (int b = 0; b < nblocks; ++b) v = add4(v, __ldg(reinterpret_cast<const float4*>(P.part_t) + b * n4 + i));
+    for (int b = 0; b < P.col_blocks; ++b) v = add4(v, __ldg(reinterpret_cast<const float4*>(P.part_t) + b * n4 + i));
     const int64_t t = i / 5;
     const int q = static_cast<int>(i - 5 * t);
     if (q == 0) reinterpret_cast<float4*>(P.gpost)[t] = v;
@@ -977,34 +975,40 @@ __global__ void __launch_bounds__(256) ckb_reduce_kernel(const ReduceParams P) {
 
 // Byte offsets of the workspace's parts and the work split.
 struct Plan {
-  size_t wt, gm, rec, hm, lo, mix, gain, w, t, bytes;
-  int tt, ntiles, per, ranges;   // stream kernel
+  size_t wt, gm, rec, hm, lo, scales, mix, gain, w, t, bytes;
+  int tt, ntiles, per, ranges, spb, nblocks;   // stream kernel
   int mix_blocks;
 };
 
-// Token tiles of tt rows in `ranges` ranges of `per` tiles: the busiest block's items x tiles x time of a
-// tile, which is about that of its tokens and 40 more (waits and fills that every slot has).
-Plan plan_of(int64_t N, int d, int sms) {
+// Columns in blocks of spb slots, token tiles of tt rows in `ranges` ranges of `per` tiles: the least time of the
+// busiest block. A slot of tt rows takes about as long as tt + 160 rows' copies, whatever tt (every thread
+// computes), a tile about two thirds of a slot more (its weights, and gu and gC at its end), an item half of one.
+Plan search_plan(int64_t N, int d, int sms) {
   Plan p{};
-  if (sms <= 0 || d <= 0 || d % SB_COLS != 0) return p;
-  const int64_t nblocks = d / SB_COLS;
+  if (sms <= 0 || d <= 0 || d % 64 != 0) return p;
   int64_t best = INT64_MAX;
   p.tt = 16;
   p.ntiles = p.per = p.ranges = 1;
-  for (int tt = SBR; N > 0 && tt >= 16; tt -= 16) {
-    const int64_t tiles = (N + tt - 1) / tt;
-    const int64_t most = std::min<int64_t>(tiles, 64);
-    for (int64_t want = 1; want <= most; ++want) {
-      const int64_t per = (tiles + want - 1) / want, ranges = (tiles + per - 1) / per;
-      const int64_t rounds = (nblocks * ranges + sms - 1) / sms;
-      // a range costs its W^T load and its gW sums, about a tile of 32 tokens
-      const int64_t cost = rounds * (per * (tt + 40) + 32);
-      if (cost < best) {
-        best = cost;
-        p.tt = tt;
-        p.ntiles = static_cast<int>(tiles);
-        p.per = static_cast<int>(per);
-        p.ranges = static_cast<int>(ranges);
+  p.spb = 2;
+  p.nblocks = d / 64;
+  for (int spb = SB_SLOTS; N > 0 && spb >= 2; spb /= 2) {
+    const int64_t nblocks = (d / 32 + spb - 1) / spb;
+    for (int tt = SBR; tt >= 16; tt -= 16) {
+      const int64_t tiles = (N + tt - 1) / tt;
+      const int64_t most = std::min<int64_t>(tiles, 64);
+      for (int64_t want = 1; want <= most; ++want) {
+        const int64_t per = (tiles + want - 1) / want, ranges = (tiles + per - 1) / per;
+        const int64_t rounds = (nblocks * ranges + sms - 1) / sms;
+        const int64_t cost = rounds * (per * (std::min(spb, d / 32) * (tt + 160) + 160) + 128);
+        if (cost < best) {
+          best = cost;
+          p.tt = tt;
+          p.ntiles = static_cast<int>(tiles);
+          p.per = static_cast<int>(per);
+          p.ranges = static_cast<int>(ranges);
+          p.spb = spb;
+          p.nblocks = static_cast<int>(nblocks);
+        }
       }
     }
   }
@@ -1021,12 +1025,27 @@ Plan plan_of(int64_t N, int d, int sms) {
   p.rec = part(n * 16);
   p.hm = part(n * 128);
   p.lo = part(n * 64);
+  p.scales = part(static_cast<size_t>(d / 32) * p.ntiles * p.tt * 8);
   p.mix = part(static_cast<size_t>(p.mix_blocks) * 128);
   p.gain = part(static_cast<size_t>(p.ranges) * 3 * d * 4);
   p.w = part(static_cast<size_t>(p.ranges) * MIXN * 4 * d * 4);
-  p.t = part(static_cast<size_t>(nblocks) * n * 80);
+  p.t = part(static_cast<size_t>(p.nblocks) * n * 80);
   p.bytes = off;
   return p;
+}
+
+// The plan of a shape is searched once per thread and change of shape.
+Plan plan_of(int64_t N, int d, int sms) {
+  thread_local Plan last{};
+  thread_local int64_t of_n = -1;
+  thread_local int of_d = 0, of_sms = 0;
+  if (N != of_n || d != of_d || sms != of_sms) {
+    last = search_plan(N, d, sms);
+    of_n = N;
+    of_d = d;
+    of_sms = sms;
+  }
+  return last;
 }
 
 // Codes: uint8 [rows][4 or 1][d], boxes of 32 columns of `rows_box` rows, 32-byte swizzle.
@@ -1078,7 +1097,8 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
       kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 2 * static_cast<int64_t>(sms))), TOKEN_WARPS * 32, 0, stream>>>(
           in, static_cast<const uint4*>(a.gy), a.pre_prev, a.post_prev, a.comb_prev, a.gain, a.mixes, wsf(p.gm),
           wsf(p.rec), reinterpret_cast<__nv_bfloat16*>(ws + p.hm), reinterpret_cast<__nv_bfloat16*>(ws + p.lo),
-          a.gpre_prev, N, d, a.norm_eps, row_dest, -0.0f);
+          a.gpre_prev, reinterpret_cast<uint2*>(ws + p.scales), static_cast<int64_t>(p.ntiles) * p.tt, N, d, a.norm_eps,
+          row_dest, -0.0f);
       return cudaGetLastError();
     };
     // a warp a token once every warp the device holds (two blocks a multiprocessor) has one
@@ -1101,8 +1121,7 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
     P.comb = a.comb_prev;
     P.rec = wsf(p.rec);
     P.gain = a.gain;
-    P.Xs = static_cast<const uint8_t*>(ck.X_scale);
-    P.Fs = static_cast<const uint8_t*>(ck.F_scale);
+    P.scales = reinterpret_cast<const uint2*>(ws + p.scales);
     P.wT = ws + p.wt;
     P.part_w = wsf(p.w);
     P.part_gain = wsf(p.gain);
@@ -1114,11 +1133,13 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
     P.ntiles = p.ntiles;
     P.per = p.per;
     P.ranges = p.ranges;
+    P.spb = p.spb;
+    P.nblocks = p.nblocks;
     P.neg_zero = -0.0f;
     P.row_dest = row_dest;
     e = cudaFuncSetAttribute(ckb_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SB_SMEM);
     if (e != cudaSuccess) return e;
-    const int items = d / SB_COLS * p.ranges;
+    const int items = p.nblocks * p.ranges;
     ckb_stream_kernel<<<std::min(items, sms), SB_THREADS, SB_SMEM, stream>>>(tx, tf, tgxp, tgy, tgx, tgf, thm, tlo, P);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -1139,6 +1160,7 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
   R.ranges = p.ranges;
   R.gain_rows = 3 * p.ranges;
   R.mix_blocks = p.mix_blocks;
+  R.col_blocks = p.nblocks;
   R.gw = (MIXN * d + 255) / 256;
   R.gg = (d / 4 + 31) / 32;
   R.gt = (N * 5 + 255) / 256;
