@@ -39,6 +39,73 @@ unsigned* status_word() {
   return g_status_ptr[dev];
 }
 
+DeviceInfo device_info() {
+  static std::mutex mu;
+  static DeviceInfo known[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DeviceInfo{0, 0};
+  std::lock_guard<std::mutex> lock(mu);
+  DeviceInfo& d = known[dev];
+  if (d.sms == 0) {
+    int sms = 0, smem = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
+      return DeviceInfo{0, 0};
+    d = DeviceInfo{sms, smem};
+  }
+  return d;
+}
+
+namespace {
+// What is known of a kernel: the devices whose shared-memory limit is set, and its registers.
+struct KernelInfo {
+  const void* kernel;
+  unsigned long long allowed;
+  int registers;
+};
+constexpr int kMaxKernels = 64;
+KernelInfo g_kernels[kMaxKernels] = {};
+std::mutex g_kernels_mu;
+KernelInfo* kernel_info(const void* kernel) {   // under g_kernels_mu; nullptr if the table is full
+  for (KernelInfo& k : g_kernels) {
+    if (k.kernel == kernel) return &k;
+    if (k.kernel == nullptr) {
+      k.kernel = kernel;
+      return &k;
+    }
+  }
+  return nullptr;
+}
+}  // namespace
+
+cudaError_t allow_shared_memory(const void* kernel) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const DeviceInfo info = device_info();
+  std::lock_guard<std::mutex> lock(g_kernels_mu);
+  KernelInfo* k = kernel_info(kernel);
+  if (k != nullptr && dev < kMaxDevices && ((k->allowed >> dev) & 1u)) return cudaSuccess;
+  // static shared memory counts too: the most that is left beside it
+  cudaFuncAttributes attr{};
+  cudaError_t r = cudaFuncGetAttributes(&attr, kernel);
+  if (r == cudaSuccess)
+    r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             info.smem - static_cast<int>(attr.sharedSizeBytes));
+  if (r == cudaSuccess && k != nullptr && dev < kMaxDevices) k->allowed |= 1ull << dev;
+  return r;
+}
+
+int kernel_registers(const void* kernel) {
+  std::lock_guard<std::mutex> lock(g_kernels_mu);
+  KernelInfo* k = kernel_info(kernel);
+  if (k != nullptr && k->registers > 0) return k->registers;
+  cudaFuncAttributes attr{};
+  if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess) return 255;
+  if (k != nullptr) k->registers = attr.numRegs;
+  return attr.numRegs;
+}
+
 unsigned long long* trace_buffer(int64_t ctas) {
   return (g_trace != nullptr && ctas <= g_trace_ctas) ? g_trace : nullptr;
 }

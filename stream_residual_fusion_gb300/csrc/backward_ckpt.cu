@@ -54,9 +54,10 @@ __device__ __forceinline__ Planes planes_of(float v) {
 
 constexpr int PREP_THREADS = 128;
 constexpr int PREP_TOKENS = PREP_THREADS / 4;
-// Sinkhorn step inputs kept a token (shared memory, 64 bytes each): all of them up to 24 rounds, every
-// second one up to 48, ...
-constexpr int PREP_KEEP = 47;
+// Sinkhorn step inputs kept a token (shared memory, 64 bytes each), at most: enough for 24 rounds where a
+// block or two a multiprocessor are all there is (the steps are one long chain), and every so many steps' where
+// more blocks fit side by side instead.
+constexpr int PREP_KEEP = 47, PREP_KEEP_MANY = 13;
 constexpr int W_HM = 128 * 128;                  // W^T hi and mid planes of 32 columns: 128 rows x 128 bytes
 constexpr int W_LO = 128 * 64;                   // lo plane
 constexpr int W_SLOT = W_HM + W_LO;
@@ -1064,10 +1065,10 @@ bool code_map(CUtensorMap* m, const void* p, int64_t N, int d, int streams, uint
 
 }  // namespace
 
-size_t bwd_ckpt_bytes(int64_t N, int d) { return plan_of(N, d, sm_count()).bytes; }
+size_t bwd_ckpt_bytes(int64_t N, int d) { return plan_of(N, d, device_info().sms).bytes; }
 
 cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cudaStream_t stream) {
-  const int sms = sm_count(), d = a.d;
+  const int sms = device_info().sms, d = a.d;
   const int64_t N = a.N;
   const Plan p = plan_of(N, d, sms);
   if (p.bytes == 0 || a.workspace_bytes < p.bytes) return cudaErrorInvalidValue;
@@ -1078,12 +1079,11 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
   const int row_dest = static_cast<int>(a.flags & 1u);
   cudaError_t e;
   {
-    const int steps = 2 * a.iters - 1, every = (steps + PREP_KEEP - 1) / PREP_KEEP;
+    const int keep = p.mix_blocks <= 2 * sms ? PREP_KEEP : PREP_KEEP_MANY;
+    const int steps = 2 * a.iters - 1, every = (steps + keep - 1) / keep;
     const int smem = (steps + every - 1) / every * PREP_THREADS * 16;
-    if (smem > 48 * 1024 - 1024) {
-      e = cudaFuncSetAttribute(ckb_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-    }
+    e = allow_shared_memory(reinterpret_cast<const void*>(ckb_prep_kernel));
+    if (e != cudaSuccess) return e;
     ckb_prep_kernel<<<p.mix_blocks + d / 32, PREP_THREADS, smem, stream>>>(
         a.mixes, a.gpre, a.gpost, a.gcomb, a.scale, a.base, a.W, wsf(p.gm), wsf(p.mix), ws + p.wt, N, d, a.iters,
         a.hc_eps, p.mix_blocks, every);
@@ -1137,7 +1137,7 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
     P.nblocks = p.nblocks;
     P.neg_zero = -0.0f;
     P.row_dest = row_dest;
-    e = cudaFuncSetAttribute(ckb_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SB_SMEM);
+    e = allow_shared_memory(reinterpret_cast<const void*>(ckb_stream_kernel));
     if (e != cudaSuccess) return e;
     const int items = p.nblocks * p.ranges;
     ckb_stream_kernel<<<std::min(items, sms), SB_THREADS, SB_SMEM, stream>>>(tx, tf, tgxp, tgy, tgx, tgf, thm, tlo, P);

@@ -58,8 +58,7 @@ __global__ void __launch_bounds__(CKP_THREADS) load_kernel(const uint2* __restri
 }
 
 int ckpt_grid(int64_t work) {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = std::max(1, device_info().sms);
   const int64_t blocks = (work + CKP_THREADS - 1) / CKP_THREADS;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(blocks, static_cast<int64_t>(sms) * 16)));
 }

@@ -179,6 +179,17 @@ struct BwdCheckpoint {
 size_t bwd_ckpt_bytes(int64_t N, int d);
 cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& c, cudaStream_t stream);
 
+// Properties of the current device, queried once; sms 0 if it cannot be.
+struct DeviceInfo {
+  int sms;
+  int smem;   // shared memory a block may have
+};
+DeviceInfo device_info();
+// Allows `kernel` all the shared memory of the current device's blocks (set once per kernel and device).
+cudaError_t allow_shared_memory(const void* kernel);
+// Registers a thread of `kernel` (queried once; 255 if that fails).
+int kernel_registers(const void* kernel);
+
 // Activation checkpoints (checkpoint.cu): bf16 rows of d features to MXFP8 and back.
 cudaError_t launch_checkpoint_save(const void* x, void* codes, void* scales, int64_t rows, int d,
                                    cudaStream_t stream);

@@ -941,29 +941,14 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const NormArgs P, int 
   }
 }
 
-struct Device {
-  int sms, smem;   // multiprocessors, shared memory a block may have
-};
-Device norm_device() {
-  int dev = 0;
-  Device v{0, 0};
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&v.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&v.smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
-    return Device{0, 0};
-  return v;
-}
-
 // Blocks of the backward, and so rows of partial sums: at most this many per multiprocessor.
 constexpr int NORM_BACK_BLOCKS = 4;
 
 template <typename K>
 cudaError_t launch_rows(K kernel, const NormArgs& a, int64_t grid, cudaStream_t stream) {
   const int smem = a.d * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel));
+  if (e != cudaSuccess) return e;
   kernel<<<static_cast<unsigned>(grid), NT, smem, stream>>>(a);
   return cudaGetLastError();
 }
@@ -980,7 +965,7 @@ int l1_room(int d) { return 12 * d; }
 // Launches a staged kernel (`kernel`, its stage sizes S) where a stage fits at all. cap: blocks per
 // multiprocessor. *ran: the launched blocks, 0 if the kernel does not take this size.
 template <typename K>
-cudaError_t launch_staged(K kernel, const NormArgs& a, int threads, const Stage& S, const Device& dev, int cap,
+cudaError_t launch_staged(K kernel, const NormArgs& a, int threads, const Stage& S, const DeviceInfo& dev, int cap,
                           int* ran, cudaStream_t stream) {
   *ran = 0;
   constexpr int kStatic = 4096;   // the kernels' static shared memory and the system's share of it, at most
@@ -990,16 +975,12 @@ cudaError_t launch_staged(K kernel, const NormArgs& a, int threads, const Stage&
   // rows and one of X, else one of each
   const int block = threads + 32;
   int per = std::max(1, std::min({cap, (room - l1_room(a.d)) / (2 * one + kStatic), 2048 / block}));
-  cudaError_t e;
-  Ring R{1, 1};
   if (per > 1) {
-    int fit = 0;
-    R = Ring{2, 2};
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * one);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, block, 2 * one);
-    if (e != cudaSuccess) return e;
-    per = std::max(1, std::min(per, fit));
+    // warps a multiprocessor's four register files hold, 16,384 registers each
+    const int held = 4 * (16384 / (32 * ((kernel_registers(reinterpret_cast<const void*>(kernel)) + 7) / 8 * 8)));
+    per = std::max(1, std::min(per, held / (block / 32)));
   }
+  Ring R{1, 1};
   const int space = room / per - (per > 1 ? kStatic : 0) - l1_room(a.d) / per;
   if (2 * one <= space) {
     R.rows = R.x = std::min(SMAX_STAGES, space / one);
@@ -1007,7 +988,7 @@ cudaError_t launch_staged(K kernel, const NormArgs& a, int threads, const Stage&
     R = Ring{2, 1};
   }
   const int smem = R.rows * S.bytes + R.x * S.xbytes;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel));
   if (e != cudaSuccess) return e;
   *ran = static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(dev.sms) * per));
   kernel<<<*ran, block, smem, stream>>>(a, R);
@@ -1015,7 +996,7 @@ cudaError_t launch_staged(K kernel, const NormArgs& a, int threads, const Stage&
 }
 
 template <int NS>
-cudaError_t forward_of(const NormArgs& a, const Device& dev, cudaStream_t stream) {
+cudaError_t forward_of(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
   const Stage stage = stage_of<NS, false, false>(a.d);
   const int most = SMAX_WARPS * 32;
   int ran = 0;
@@ -1031,7 +1012,7 @@ cudaError_t forward_of(const NormArgs& a, const Device& dev, cudaStream_t stream
 }
 
 template <int NS, bool CK>
-cudaError_t backward_of(const NormArgs& a, const Device& dev, int* rows, cudaStream_t stream) {
+cudaError_t backward_of(const NormArgs& a, const DeviceInfo& dev, int* rows, cudaStream_t stream) {
   *rows = 0;
   // bulk copies of a row of codes take whole 16-byte units
   if (!CK || a.d % 16 == 0) {
@@ -1054,7 +1035,7 @@ cudaError_t backward_of(const NormArgs& a, const Device& dev, int* rows, cudaStr
 }  // namespace
 
 cudaError_t launch_norm_step(const NormArgs& args, cudaStream_t stream) {
-  const Device dev = norm_device();
+  const DeviceInfo dev = device_info();
   NormArgs a = args;
   a.status = status_word();
   if (dev.sms <= 0 || a.status == nullptr) return cudaErrorInvalidDevice;
@@ -1062,11 +1043,11 @@ cudaError_t launch_norm_step(const NormArgs& args, cudaStream_t stream) {
 }
 
 int norm_backward_rows(int64_t N) {
-  return static_cast<int>(std::min<int64_t>(N, NORM_BACK_BLOCKS * static_cast<int64_t>(norm_device().sms)));
+  return static_cast<int>(std::min<int64_t>(N, NORM_BACK_BLOCKS * static_cast<int64_t>(device_info().sms)));
 }
 
 cudaError_t launch_norm_step_backward(const NormArgs& args, cudaStream_t stream) {
-  const Device dev = norm_device();
+  const DeviceInfo dev = device_info();
   NormArgs a = args;
   a.status = status_word();
   if (dev.sms <= 0 || a.status == nullptr) return cudaErrorInvalidDevice;

@@ -320,51 +320,54 @@ def fused_step_backward(X, F, Xp, mixes, pre_prev, post_prev, comb_prev, W, scal
 # ---------------------------------------------------------------------------------------------
 # activation checkpoints and the norm step
 
-def _need_all(spec):
-    """Checks (tensor, dtype, shape, name) entries: type, device, contiguity and shape, all on the
-    current device. Entries whose tensor is None are left out."""
-    current = torch.cuda.current_device()
+def _need_all(spec, device):
+    """Checks (tensor, dtype, shape, name) entries: type, contiguity, shape, and that they are on CUDA
+    device number `device`. Entries whose tensor is None are left out."""
     for t, dtype, shape, name in spec:
         if t is None:
             continue
-        if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda
-                and t.is_contiguous() and t.get_device() == current):
+        if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == device
+                and t.is_contiguous()):
             continue
         _need(t, dtype, name)
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.get_device() != current:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{current}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _fill(out, shapes, like, stream):
-    """`out` with the missing ones of `shapes` ({name: (shape, dtype)}) allocated on the device of
-    `like`, the given ones checked. New tensors belong to `stream` (the current one if None): the caching
-    allocator hands their memory out again only behind the work queued there."""
+def _made(out, likes, device, stream):
+    """The outputs `likes` ({name: a tensor of its shape and type}) as new tensors, or as `out` gives them
+    (checked). New tensors belong to `stream` (the current one if None): the caching allocator hands their
+    memory out again only behind the work queued there."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return _fill(out, shapes, like, None)
-    o = dict(out) if out else {}
-    given = [(o[k], *reversed(shapes[k]), k) for k in shapes if o.get(k) is not None] if o else ()
-    _need_all(given)
-    for k, (shape, dtype) in shapes.items():
+            return _made(out, likes, device, None)
+    if not out:
+        return {k: torch.empty_like(v) for k, v in likes.items()}
+    o = dict(out)
+    _need_all([(o.get(k), v.dtype, v.shape, k) for k, v in likes.items()], device)
+    for k, v in likes.items():
         if o.get(k) is None:
-            o[k] = like.new_empty(shape, dtype=dtype)
+            o[k] = torch.empty_like(v)
     return o
 
 
-def _scratch(nbytes, like, stream):
-    return _fill(None, {"w": ((max(1, nbytes),), torch.uint8)}, like, stream)["w"]
+def _new(shape, dtype, device, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _queue(stream):
+def _queue(device, stream):
     """The stream's handle, the current one's if None."""
     if stream is None:   # torch.cuda.current_stream().cuda_stream without the stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream
 
 
@@ -375,22 +378,34 @@ def _scale_shape(shape):
 def checkpoint_save(x, out=None, stream=None):
     """mhc_checkpoint_save: bf16 x [..., d] -> (codes uint8 [..., d], scales uint8 [..., ceil(d/32)]),
     the MXFP8 checkpoint of its rows. `out` is a (codes, scales) pair to write to."""
-    _need_all([(x, torch.bfloat16, x.shape, "x")])
-    o = _fill(None if out is None else dict(zip(("codes", "scales"), out)),
-              {"codes": (x.shape, torch.uint8), "scales": (_scale_shape(x.shape), torch.uint8)}, x, stream)
-    d = x.shape[-1]
-    _check(lib.mhc_checkpoint_save(_at(x), _at(o["codes"]), _at(o["scales"]), math.prod(x.shape[:-1]), d,
-                                   _queue(stream)), "mhc_checkpoint_save")
-    return o["codes"], o["scales"]
+    device = torch.cuda.current_device()
+    shape = x.shape
+    _need_all(((x, torch.bfloat16, shape, "x"),), device)
+    d = shape[-1]
+    if out is None:
+        codes = _new(shape, torch.uint8, x.device, stream)
+        scales = _new(_scale_shape(shape), torch.uint8, x.device, stream)
+    else:
+        codes, scales = out
+        _need_all(((codes, torch.uint8, shape, "codes"), (scales, torch.uint8, _scale_shape(shape), "scales")),
+                  device)
+    rc = lib.mhc_checkpoint_save(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), x.numel() // max(d, 1), d,
+                                 _queue(device, stream))
+    _check(rc, "mhc_checkpoint_save")
+    return codes, scales
 
 
 def checkpoint_load(codes, scales, out=None, stream=None):
     """mhc_checkpoint_load: the bf16 rows [..., d] that a checkpoint stands for."""
-    _need_all([(codes, torch.uint8, codes.shape, "codes"),
-               (scales, torch.uint8, _scale_shape(codes.shape), "scales")])
-    x = _fill({"x": out}, {"x": (codes.shape, torch.bfloat16)}, codes, stream)["x"]
-    _check(lib.mhc_checkpoint_load(_at(codes), _at(scales), _at(x), math.prod(codes.shape[:-1]),
-                                   codes.shape[-1], _queue(stream)), "mhc_checkpoint_load")
+    device = torch.cuda.current_device()
+    shape = codes.shape
+    _need_all(((codes, torch.uint8, shape, "codes"), (scales, torch.uint8, _scale_shape(shape), "scales"),
+               (out, torch.bfloat16, shape, "out")), device)
+    d = shape[-1]
+    x = _new(shape, torch.bfloat16, codes.device, stream) if out is None else out
+    rc = lib.mhc_checkpoint_load(codes.data_ptr(), scales.data_ptr(), x.data_ptr(), codes.numel() // max(d, 1),
+                                 d, _queue(device, stream))
+    _check(rc, "mhc_checkpoint_load")
     return x
 
 
@@ -404,35 +419,40 @@ def fused_step_backward_ckpt(X_codes, X_scale, F_codes, F_scale, mixes, pre_prev
     """mhc_fused_step_backward_ckpt: fused_step_backward from checkpoints of X and F
     (checkpoint_save), without X'. Same returns."""
     N, n, d = X_codes.shape
+    device = torch.cuda.current_device()
     u8, bf, fp = torch.uint8, torch.bfloat16, torch.float32
-    _need_all([(X_codes, u8, (N, n, d), "X_codes"), (X_scale, u8, _scale_shape((N, n, d)), "X_scale"),
-               (F_codes, u8, (N, d), "F_codes"), (F_scale, u8, _scale_shape((N, d)), "F_scale"),
+    nb = -(-d // MX_BLOCK)
+    _need_all(((X_codes, u8, (N, n, d), "X_codes"), (X_scale, u8, (N, n, nb), "X_scale"),
+               (F_codes, u8, (N, d), "F_codes"), (F_scale, u8, (N, nb), "F_scale"),
                (mixes, fp, (N, MIX), "mixes"), (pre_prev, fp, (N, n), "pre_prev"),
                (post_prev, fp, (N, n), "post_prev"), (comb_prev, fp, (N, n, n), "comb_prev"),
                (W, fp, (MIX, n * d), "W"), (scale, fp, (3,), "scale"), (base, fp, (MIX,), "base"),
                (gain, fp, (d,), "gain"), (gXp, bf, (N, n, d), "gXp"), (gy, bf, (N, d), "gy"),
-               (gpre, fp, (N, n), "gpre"), (gpost, fp, (N, n), "gpost"), (gcomb, fp, (N, n, n), "gcomb")])
-    o = _fill(out, {"gX": ((N, n, d), bf), "gF": ((N, d), bf), "gpre_prev": ((N, n), fp),
-                    "gpost_prev": ((N, n), fp), "gcomb_prev": ((N, n, n), fp), "gW": ((MIX, n * d), fp),
-                    "gbase": ((MIX,), fp), "gscale": ((3,), fp), "ggain": ((d,), fp)}, gXp, stream)
+               (gpre, fp, (N, n), "gpre"), (gpost, fp, (N, n), "gpost"), (gcomb, fp, (N, n, n), "gcomb")), device)
+    o = _made(out, {"gX": gXp, "gF": gy, "gpre_prev": pre_prev, "gpost_prev": post_prev, "gcomb_prev": comb_prev,
+                    "gW": W, "gbase": base, "gscale": scale, "ggain": gain}, device, stream)
     if workspace is None:
-        workspace = _scratch(backward_ckpt_workspace_bytes(N, d, n), gXp, stream)
+        workspace = _new(max(1, backward_ckpt_workspace_bytes(N, d, n)), u8, gXp.device, stream)
     rc = lib.mhc_fused_step_backward_ckpt(
-        _at(X_codes), _at(X_scale), _at(F_codes), _at(F_scale), _at(mixes), _at(pre_prev),
-        _at(post_prev), _at(comb_prev), _at(W), _at(scale), _at(base), _at(gain), _at(gXp), _at(gy),
-        _at(gpre), _at(gpost), _at(gcomb), _at(o["gX"]), _at(o["gF"]), _at(o["gpre_prev"]),
-        _at(o["gpost_prev"]), _at(o["gcomb_prev"]), _at(o["gW"]), _at(o["gbase"]), _at(o["gscale"]),
-        _at(o["ggain"]), N, n, d, iters, hc_eps, norm_eps, flags, _at(workspace),
-        workspace.numel() * workspace.element_size(), _queue(stream))
+        X_codes.data_ptr(), X_scale.data_ptr(), F_codes.data_ptr(), F_scale.data_ptr(), mixes.data_ptr(),
+        pre_prev.data_ptr(), post_prev.data_ptr(), comb_prev.data_ptr(), W.data_ptr(), scale.data_ptr(),
+        base.data_ptr(), gain.data_ptr(), gXp.data_ptr(), gy.data_ptr(), gpre.data_ptr(), gpost.data_ptr(),
+        gcomb.data_ptr(), o["gX"].data_ptr(), o["gF"].data_ptr(), o["gpre_prev"].data_ptr(),
+        o["gpost_prev"].data_ptr(), o["gcomb_prev"].data_ptr(), o["gW"].data_ptr(), o["gbase"].data_ptr(),
+        o["gscale"].data_ptr(), o["ggain"].data_ptr(), N, n, d, iters, hc_eps, norm_eps, flags,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _queue(device, stream))
     _check(rc, "mhc_fused_step_backward_ckpt")
     return o
 
 
 def _norm_shapes(N, n, d, gain_post, gain_pre, gate, pre, post, comb, flags):
-    rows = () if flags & WEIGHTS_SHARED else (N,)
     fp = torch.float32
-    return [(gate, torch.bfloat16, (N, d), "gate"), (pre, fp, (*rows, n), "pre"), (post, fp, (*rows, n), "post"),
-            (comb, fp, (*rows, n, n), "comb"), (gain_post, fp, (d,), "gain_post"), (gain_pre, fp, (d,), "gain_pre")]
+    rows = () if flags & WEIGHTS_SHARED else (N,)
+    spec = [(gain_post, fp, (d,), "gain_post"), (gain_pre, fp, (d,), "gain_pre"),
+            (gate, torch.bfloat16, (N, d), "gate")]
+    if pre is not None or post is not None or comb is not None:
+        spec += [(pre, fp, (*rows, n), "pre"), (post, fp, (*rows, n), "post"), (comb, fp, (*rows, n, n), "comb")]
+    return spec
 
 
 def norm_step(X, F, gain_post, gain_pre, *, gate=None, pre=None, post=None, comb=None, res_scale=1.0,
@@ -441,13 +461,14 @@ def norm_step(X, F, gain_post, gain_pre, *, gate=None, pre=None, post=None, comb
     residual scale, the residual streams X [N, n, d] (n = 1 or 4) under given weights, and the norm
     before the next block (gain_pre). Returns dict with Xp, y."""
     N, n, d = X.shape
+    device = torch.cuda.current_device()
     bf = torch.bfloat16
-    _need_all([(X, bf, (N, n, d), "X"), (F, bf, (N, d), "F"),
-               *_norm_shapes(N, n, d, gain_post, gain_pre, gate, pre, post, comb, flags)])
-    o = _fill(out, {"Xp": ((N, n, d), bf), "y": ((N, d), bf)}, X, stream)
-    rc = lib.mhc_norm_step(_at(X), _at(F), _at(gate), _at(pre), _at(post), _at(comb), _at(gain_post),
-                           _at(gain_pre), _at(o["Xp"]), _at(o["y"]), N, n, d, res_scale, norm_eps, flags,
-                           _queue(stream))
+    _need_all(((X, bf, (N, n, d), "X"), (F, bf, (N, d), "F"),
+               *_norm_shapes(N, n, d, gain_post, gain_pre, gate, pre, post, comb, flags)), device)
+    o = _made(out, {"Xp": X, "y": F}, device, stream)
+    rc = lib.mhc_norm_step(X.data_ptr(), F.data_ptr(), _at(gate), _at(pre), _at(post), _at(comb), _at(gain_post),
+                           gain_pre.data_ptr(), o["Xp"].data_ptr(), o["y"].data_ptr(), N, n, d, res_scale,
+                           norm_eps, flags, _queue(device, stream))
     _check(rc, "mhc_norm_step")
     return o
 
@@ -458,25 +479,25 @@ def norm_step_backward_workspace_bytes(N: int, d: int, n: int = N_STREAMS) -> in
 
 def _norm_step_backward(call, where, saved, N, n, d, gXp, gy, gain_post, gain_pre, gate, pre, post, comb,
                         res_scale, norm_eps, flags, out, workspace, stream):
-    bf, fp = torch.bfloat16, torch.float32
-    _need_all([*saved, (gXp, bf, (N, n, d), "gXp"), (gy, bf, (N, d), "gy"),
-               *_norm_shapes(N, n, d, gain_post, gain_pre, gate, pre, post, comb, flags)])
-    shapes = {"gX": ((N, n, d), bf), "gF": ((N, d), bf), "ggain_pre": ((d,), fp)}
+    device = torch.cuda.current_device()
+    bf = torch.bfloat16
+    _need_all((*saved, (gXp, bf, (N, n, d), "gXp"), (gy, bf, (N, d), "gy"),
+               *_norm_shapes(N, n, d, gain_post, gain_pre, gate, pre, post, comb, flags)), device)
+    likes = {"gX": gXp, "gF": gy, "ggain_pre": gain_pre}
     if gain_post is not None:
-        shapes["ggain_post"] = ((d,), fp)
+        likes["ggain_post"] = gain_post
     if gate is not None:
-        shapes["ggate"] = ((N, d), bf)
+        likes["ggate"] = gate
     if pre is not None:
-        rows = () if flags & WEIGHTS_SHARED else (N,)
-        shapes.update(gpre=((*rows, n), fp), gpost=((*rows, n), fp), gcomb=((*rows, n, n), fp))
-    o = _fill(out, shapes, gXp, stream)
+        likes.update(gpre=pre, gpost=post, gcomb=comb)
+    o = _made(out, likes, device, stream)
     if workspace is None:
-        workspace = _scratch(norm_step_backward_workspace_bytes(N, d, n), gXp, stream)
-    rc = call(*[_at(t) for t, _, _, _ in saved], _at(gate), _at(pre), _at(post), _at(comb),
-              _at(gain_post), _at(gain_pre), _at(gXp), _at(gy), _at(o["gX"]), _at(o["gF"]),
+        workspace = _new(max(1, norm_step_backward_workspace_bytes(N, d, n)), torch.uint8, gXp.device, stream)
+    rc = call(*[t.data_ptr() for t, _, _, _ in saved], _at(gate), _at(pre), _at(post), _at(comb), _at(gain_post),
+              gain_pre.data_ptr(), gXp.data_ptr(), gy.data_ptr(), o["gX"].data_ptr(), o["gF"].data_ptr(),
               _at(o.get("ggate")), _at(o.get("gpre")), _at(o.get("gpost")), _at(o.get("gcomb")),
-              _at(o.get("ggain_post")), _at(o["ggain_pre"]), N, n, d, res_scale, norm_eps, flags,
-              _at(workspace), workspace.numel() * workspace.element_size(), _queue(stream))
+              _at(o.get("ggain_post")), o["ggain_pre"].data_ptr(), N, n, d, res_scale, norm_eps, flags,
+              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _queue(device, stream))
     _check(rc, where)
     return o
 
@@ -486,7 +507,7 @@ def norm_step_backward(X, F, gXp, gy, gain_post, gain_pre, *, gate=None, pre=Non
     """mhc_norm_step_backward: gradients of norm_step from gXp, gy (those of Xp and y). Returns dict
     with gX, gF, ggain_pre, and ggate, ggain_post, gpre, gpost, gcomb for what norm_step was given."""
     N, n, d = X.shape
-    saved = [(X, torch.bfloat16, (N, n, d), "X"), (F, torch.bfloat16, (N, d), "F")]
+    saved = ((X, torch.bfloat16, (N, n, d), "X"), (F, torch.bfloat16, (N, d), "F"))
     return _norm_step_backward(lib.mhc_norm_step_backward, "mhc_norm_step_backward", saved, N, n, d, gXp, gy,
                                gain_post, gain_pre, gate, pre, post, comb, res_scale, norm_eps, flags, out,
                                workspace, stream)
@@ -497,9 +518,9 @@ def norm_step_backward_ckpt(X_codes, X_scale, F_codes, F_scale, gXp, gy, gain_po
                             workspace=None, stream=None):
     """mhc_norm_step_backward_ckpt: norm_step_backward from checkpoints of X and F (checkpoint_save)."""
     N, n, d = X_codes.shape
-    u8 = torch.uint8
-    saved = [(X_codes, u8, (N, n, d), "X_codes"), (X_scale, u8, _scale_shape((N, n, d)), "X_scale"),
-             (F_codes, u8, (N, d), "F_codes"), (F_scale, u8, _scale_shape((N, d)), "F_scale")]
+    u8, nb = torch.uint8, -(-d // MX_BLOCK)
+    saved = ((X_codes, u8, (N, n, d), "X_codes"), (X_scale, u8, (N, n, nb), "X_scale"),
+             (F_codes, u8, (N, d), "F_codes"), (F_scale, u8, (N, nb), "F_scale"))
     return _norm_step_backward(lib.mhc_norm_step_backward_ckpt, "mhc_norm_step_backward_ckpt", saved, N, n, d,
                                gXp, gy, gain_post, gain_pre, gate, pre, post, comb, res_scale, norm_eps, flags,
                                out, workspace, stream)
