@@ -31,7 +31,14 @@ __device__ __forceinline__ float group_sums(float (&v)[V], float* scratch, int w
   if (lane < V) scratch[warp * V + lane] = mine;
   named_bar_sync(1, nthreads);
   float t = 0.f;
-  for (int w = 0; w < warps; ++w) t += scratch[w * V + (lane & (V - 1))];
+  if (V <= 2) {   // at most 16 warps: every sum in a lane of its own, added by shuffles
+    t = lane < warps * V ? scratch[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o >= V; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
+  } else {
+#pragma unroll 4
+    for (int w = 0; w < warps; ++w) t += scratch[w * V + (lane & (V - 1))];
+  }
   return t;
 }
 __device__ __forceinline__ float lane_value(float v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }

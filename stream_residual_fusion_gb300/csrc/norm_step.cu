@@ -360,6 +360,17 @@ __host__ __device__ constexpr Stage stage_of(int d) {
 struct Ring {
   int rows, x;
 };
+// A place in a ring, walked without divisions: its stage, and the parity of its use.
+struct Place {
+  int stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+};
 struct Barriers {
   uint64_t full[SMAX_STAGES], empty[SMAX_STAGES], xfull[SMAX_STAGES], xempty[SMAX_STAGES];
 };
@@ -420,14 +431,16 @@ __device__ __forceinline__ bool produce(const NormArgs& P, uint8_t* sm, Barriers
   const uint32_t bytes = saved + (P.gate ? row : 0u) + (BACK ? (NS + 1) * row : 0u) + (NS == 4 ? 96u : 0u);
   uint8_t* xs = sm + R.rows * S.bytes;
   bool late = false;
-  auto free_of = [&](uint64_t* empty, int i, int stages) {
-    if (i >= stages && !mbar_wait(&empty[i % stages], ((i / stages) - 1) & 1, late ? 0ull : NORM_WAIT_NS)) late = true;
+  // the first use of a stage waits for nobody, a later one for the release of the use before it
+  auto free_of = [&](uint64_t* empty, const Place& p, bool used) {
+    if (used && !mbar_wait(&empty[p.stage], p.parity ^ 1u, late ? 0ull : NORM_WAIT_NS)) late = true;
   };
-  int i = 0;
-  for (int64_t t = blockIdx.x; t < P.N; t += gridDim.x, ++i) {
-    const int b = i % R.rows, x = i % R.x;
+  Place rp, xp;
+  bool rused = false, xused = false;
+  for (int64_t t = blockIdx.x; t < P.N; t += gridDim.x) {
+    const int b = rp.stage, x = xp.stage;
     auto at = [&](const void* p, int64_t n) { return static_cast<const uint8_t*>(p) + t * n; };
-    free_of(B.empty, i, R.rows);
+    free_of(B.empty, rp, rused);
     uint8_t* st = sm + b * S.bytes;
     mbar_arrive_expect_tx(&B.full[b], bytes);
     bulk_load_hint(st, at(P.F, saved), saved, &B.full[b], pol);
@@ -442,9 +455,13 @@ __device__ __forceinline__ bool produce(const NormArgs& P, uint8_t* sm, Barriers
       bulk_load_hint(st + S.w + 16, P.post + wt * 4, 16, &B.full[b], pol);
       bulk_load_hint(st + S.w + 32, P.comb + wt * 16, 64, &B.full[b], pol);
     }
-    free_of(B.xempty, i, R.x);
+    free_of(B.xempty, xp, xused);
     mbar_arrive_expect_tx(&B.xfull[x], NS * saved);
     bulk_load_hint(xs + x * S.xbytes, at(P.X, static_cast<int64_t>(NS) * saved), NS * saved, &B.xfull[x], pol);
+    rp.next(R.rows);
+    xp.next(R.x);
+    rused |= rp.stage == 0;
+    xused |= xp.stage == 0;
   }
   return late;
 }
@@ -470,9 +487,7 @@ __device__ __forceinline__ void gate_gain(const NormArgs& P, const uint8_t* gate
   for (int i = 0; i < 4; ++i) sa.v[i] = mul2(both(P.res_scale), a.v[i]);
 }
 
-__device__ __forceinline__ float inv_rms(float sum, float d, float eps) {
-  return __frsqrt_rn(__fdiv_rn(sum, d) + eps);
-}
+__device__ __forceinline__ float inv_rms(float sum, float inv_d, float eps) { return rsqrtf(fmaf(sum, inv_d, eps)); }
 
 template <int NS, int CH>
 __global__ void __launch_bounds__((SMAX_WARPS + 1) * 32, 1) norm_step_staged(const NormArgs P, Ring R) {
@@ -482,14 +497,14 @@ __global__ void __launch_bounds__((SMAX_WARPS + 1) * 32, 1) norm_step_staged(con
   const Stage S = stage_of<NS, false, false>(P.d);
   const int warps = blockDim.x / 32 - 1, T = warps * 32, lane = threadIdx.x & 31;
   const int chunks = P.d / 8;
-  const float fd = static_cast<float>(P.d);
+  const float inv_d = 1.0f / static_cast<float>(P.d);
   bool late = false;
   init_barriers(B, R, warps);
   if (static_cast<int>(threadIdx.x) >= T) {
     if (lane == 0) late = produce<NS, false, false>(P, sm, B, R);
   } else {
-    auto wait = [&](uint64_t* full, int i, int stages) {
-      if (!mbar_wait(&full[i % stages], (i / stages) & 1, late ? 0ull : NORM_WAIT_NS)) late = true;
+    auto wait = [&](uint64_t* full, const Place& p) {
+      if (!mbar_wait(&full[p.stage], p.parity, late ? 0ull : NORM_WAIT_NS)) late = true;
     };
     auto sum_f = [&](const uint8_t* st) {
       f2 s{0.f, 0.f};
@@ -506,16 +521,17 @@ __global__ void __launch_bounds__((SMAX_WARPS + 1) * 32, 1) norm_step_staged(con
     // one barrier a token: the sum of yh^2 and the next token's of F^2 go together
     float r = 1.f;
     if (P.gain_post && blockIdx.x < P.N) {
-      wait(B.full, 0, R.rows);
+      wait(B.full, Place{});
       float v[2] = {0.f, sum_f(sm)};
-      r = inv_rms(lane_value(group_sums<2>(v, scratch[1], warps, T), 1), fd, P.eps);
+      r = inv_rms(lane_value(group_sums<2>(v, scratch[1], warps, T), 1), inv_d, P.eps);
     }
+    Place rp, xp;
     int n = 0;
     for (int64_t t = blockIdx.x; t < P.N; t += gridDim.x, ++n) {
-      const uint8_t* st = sm + (n % R.rows) * S.bytes;
-      const uint8_t* xt = sm + R.rows * S.bytes + (n % R.x) * S.xbytes;
-      wait(B.full, n, R.rows);
-      wait(B.xfull, n, R.x);
+      const uint8_t* st = sm + rp.stage * S.bytes;
+      const uint8_t* xt = sm + R.rows * S.bytes + xp.stage * S.xbytes;
+      wait(B.full, rp);
+      wait(B.xfull, xp);
       Weights2<NS> w;
       if constexpr (NS == 4) {
         w = stage_weights<NS>(st + S.w, (P.flags & 1u) != 0);
@@ -553,17 +569,19 @@ __global__ void __launch_bounds__((SMAX_WARPS + 1) * 32, 1) norm_step_staged(con
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&B.empty[n % R.rows]);
-        mbar_arrive(&B.xempty[n % R.x]);
+        mbar_arrive(&B.empty[rp.stage]);
+        mbar_arrive(&B.xempty[xp.stage]);
       }
+      rp.next(R.rows);
+      xp.next(R.x);
       float v[2] = {s.x + s.y, 0.f};
       if (P.gain_post && t + gridDim.x < P.N) {
-        wait(B.full, n + 1, R.rows);
-        v[1] = sum_f(sm + ((n + 1) % R.rows) * S.bytes);
+        wait(B.full, rp);
+        v[1] = sum_f(sm + rp.stage * S.bytes);
       }
       const float tot = group_sums<2>(v, scratch[n & 1], warps, T);
-      const float ry = inv_rms(lane_value(tot, 0), fd, P.eps);
-      if (P.gain_post) r = inv_rms(lane_value(tot, 1), fd, P.eps);
+      const float ry = inv_rms(lane_value(tot, 0), inv_d, P.eps);
+      if (P.gain_post) r = inv_rms(lane_value(tot, 1), inv_d, P.eps);
 #pragma unroll
       for (int q = 0; q < CH; ++q) {
         const int c = static_cast<int>(threadIdx.x) + q * T;
@@ -634,7 +652,7 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
   const int warps = blockDim.x / 32 - 1, T = warps * 32, lane = threadIdx.x & 31;
   const int units = P.d / 4, blocks = (P.d + MX_BLOCK - 1) / MX_BLOCK;
   const int srow = P.d * (CK ? 1 : 2);   // bytes of a saved row
-  const float fd = static_cast<float>(P.d);
+  const float inv_d = 1.0f / static_cast<float>(P.d);
   const bool row_dest = (P.flags & 1u) != 0, shared = (P.flags & FLAG_WEIGHTS_SHARED) != 0;
   const bool sigmoid = (P.flags & FLAG_GATE_SIGMOID) != 0;
   bool late = false;
@@ -642,8 +660,8 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
   if (static_cast<int>(threadIdx.x) >= T) {
     if (lane == 0) late = produce<NS, CK, true>(P, sm, B, R);
   } else {
-    auto wait = [&](uint64_t* full, int i, int stages) {
-      if (!mbar_wait(&full[i % stages], (i / stages) & 1, late ? 0ull : NORM_WAIT_NS)) late = true;
+    auto wait = [&](uint64_t* full, const Place& p) {
+      if (!mbar_wait(&full[p.stage], p.parity, late ? 0ull : NORM_WAIT_NS)) late = true;
     };
     // scale codes of a token's units (X's streams, low byte first; F), read a token ahead
     struct Codes {
@@ -705,14 +723,16 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
     // With more than one stage the sum of the next token's F^2 goes with this one's last sum.
     const bool ahead = R.rows > 1;
     float r = 1.f;
+    Place rp, xp;
     int n = 0;
     for (int64_t t = blockIdx.x; t < P.N; t += gridDim.x, ++n) {
-      const uint8_t* st = sm + (n % R.rows) * S.bytes;
-      const uint8_t* xt = sm + R.rows * S.bytes + (n % R.x) * S.xbytes;
-      wait(B.full, n, R.rows);
+      const int stage = rp.stage;
+      const uint8_t* st = sm + stage * S.bytes;
+      const uint8_t* xt = sm + R.rows * S.bytes + xp.stage * S.xbytes;
+      wait(B.full, rp);
       if (P.gain_post && (n == 0 || !ahead)) {
         float v[1] = {sum_f(st, sc)};
-        r = inv_rms(group_sums<1>(v, scratch1, warps, T), fd, P.eps);
+        r = inv_rms(group_sums<1>(v, scratch1, warps, T), inv_d, P.eps);
       }
       scales(t + gridDim.x, sn);
       Weights<NS> w;
@@ -736,7 +756,7 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
 #pragma unroll
         for (int k = 0; k < NS; ++k) beta[j] = fmaf(w.cc[j][k], w.p[k], beta[j]);
       }
-      wait(B.xfull, n, R.x);
+      wait(B.xfull, xp);
       C4 yh[UN];
       float tot;
       {
@@ -787,11 +807,12 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.xempty[n % R.x]);
+        if (lane == 0) mbar_arrive(&B.xempty[xp.stage]);
+        xp.next(R.x);
         tot = group_sums<V>(v, scratch2[n & 1], warps, T);
       }
-      const float ry = inv_rms(lane_value(tot, 0), fd, P.eps);
-      const float tau = ry * ry * ry * lane_value(tot, 1) / fd;
+      const float ry = inv_rms(lane_value(tot, 0), inv_d, P.eps);
+      const float tau = ry * ry * ry * lane_value(tot, 1) * inv_d;
       if (P.pre && threadIdx.x < 32) {
         const float e = ry * tot - tau * __shfl_down_sync(0xffffffffu, tot, NS + 1);   // lanes IE ..: e_z, e_j
         const float ez = lane_value(e, IE);
@@ -866,12 +887,13 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
         if (P.gate) store4(P.ggate, t * units + u, gg);
       }
       float v[2] = {s, 0.f};
+      rp.next(R.rows);
       if (P.gain_post && ahead && t + gridDim.x < P.N) {
-        wait(B.full, n + 1, R.rows);
-        v[1] = sum_f(sm + ((n + 1) % R.rows) * S.bytes, sn);
+        wait(B.full, rp);
+        v[1] = sum_f(sm + rp.stage * S.bytes, sn);
       }
       const float tot3 = P.gain_post ? group_sums<2>(v, scratch3, warps, T) : 0.f;
-      const float cf = P.gain_post ? r * r * r * lane_value(tot3, 0) / fd : 0.f;
+      const float cf = P.gain_post ? r * r * r * lane_value(tot3, 0) * inv_d : 0.f;
 #pragma unroll
       for (int q = 0; q < UN; ++q) {
         const int u = static_cast<int>(threadIdx.x) + q * T;
@@ -883,8 +905,8 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
         store4(P.gF, t * units + u, o);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&B.empty[n % R.rows]);
-      if (P.gain_post) r = inv_rms(lane_value(tot3, 1), fd, P.eps);
+      if (lane == 0) mbar_arrive(&B.empty[stage]);
+      if (P.gain_post) r = inv_rms(lane_value(tot3, 1), inv_d, P.eps);
       if constexpr (CK) {
 #pragma unroll
         for (int q = 0; q < UN; ++q) sc[q] = sn[q];
