@@ -274,7 +274,10 @@ int backward_common(const BwdArgs& a, int n, const BwdCheckpoint* c, void* strea
   return cuda_code(c ? launch_backward_ckpt(a, *c, s) : launch_backward(a, s));
 }
 
-constexpr int64_t kMaxRows = int64_t(1) << 40;   // rows of a checkpoint
+// Rows of a checkpoint of width d: what one grid covers (16 TB of codes).
+bool rows_ok(int64_t rows, int d) {
+  return rows >= 0 && d > 0 && d % 8 == 0 && rows <= (int64_t(1) << 44) / ((static_cast<int64_t>(d) + 31) / 32 * 32);
+}
 
 // Shape, flags, weights and parameters of a norm step (either direction).
 int check_norm(const NormArgs& a) {
@@ -805,12 +808,12 @@ int mhc_fused_step_backward_ckpt(const void* X_codes, const void* X_scale, const
 // Activation checkpoints.
 
 size_t mhc_checkpoint_scale_bytes(int64_t rows, int d) {
-  if (rows < 0 || rows > kMaxRows || d <= 0 || d % 8 != 0) return 0;
+  if (!rows_ok(rows, d)) return 0;
   return static_cast<size_t>(rows) * ((static_cast<size_t>(d) + 31) / 32);
 }
 
 int mhc_checkpoint_save(const void* x, void* codes, void* scales, int64_t rows, int d, void* stream) {
-  if (rows < 0 || rows > kMaxRows || d <= 0 || d % 8 != 0) return MHC_ERR_SHAPE;
+  if (!rows_ok(rows, d)) return MHC_ERR_SHAPE;
   if (rows == 0) return MHC_OK;
   if (!x || !codes || !scales) return MHC_ERR_NULL;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MHC_ERR_ALIGN;
@@ -822,7 +825,7 @@ int mhc_checkpoint_save(const void* x, void* codes, void* scales, int64_t rows, 
 }
 
 int mhc_checkpoint_load(const void* codes, const void* scales, void* x, int64_t rows, int d, void* stream) {
-  if (rows < 0 || rows > kMaxRows || d <= 0 || d % 8 != 0) return MHC_ERR_SHAPE;
+  if (!rows_ok(rows, d)) return MHC_ERR_SHAPE;
   if (rows == 0) return MHC_OK;
   if (!x || !codes || !scales) return MHC_ERR_NULL;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MHC_ERR_ALIGN;

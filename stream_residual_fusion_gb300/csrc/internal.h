@@ -225,6 +225,7 @@ struct NormArgs {
   float* ggain_pre;
   float* partial;           // norm_backward_rows(N) rows of norm_partial_floats(d)
   unsigned* status;         // the library's status word
+  float neg_zero;           // -0, only known at run time
   int64_t N;
   int n;
   int d;

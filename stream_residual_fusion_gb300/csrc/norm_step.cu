@@ -618,14 +618,47 @@ __device__ __forceinline__ Row4<CK> saved4(const uint8_t* p, int u, uint32_t cod
   else return row4(p, u);
 }
 __device__ __forceinline__ void store4(void* p, int64_t u, const uint32_t (&w)[2]) {
-  reinterpret_cast<uint2*>(p)[u] = make_uint2(w[0], w[1]);
+  // past the L1, which keeps the gains
+  asm volatile("st.global.L1::no_allocate.v2.b32 [%0], {%1, %2};" ::"l"(reinterpret_cast<uint2*>(p) + u), "r"(w[0]),
+               "r"(w[1]));
 }
 struct C4 {
   f2 v[2];
 };
 __device__ __forceinline__ C4 gain4(const float* g, int u) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(g) + u);
+  float4 a;
+  asm("ld.global.nc.L1::evict_last.v4.f32 {%0, %1, %2, %3}, [%4];"
+      : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w)
+      : "l"(reinterpret_cast<const float4*>(g) + u));
   return C4{{f2{a.x, a.y}, f2{a.z, a.w}}};
+}
+
+// D += A B on the warp's tensor cores: A 16 x 16 (rows 8..15 zero), B 16 x 8, bf16; D fp32.
+__device__ __forceinline__ void mma_rows8(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %5}, {%7, %8}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1));
+}
+
+// This warp's share of gXp_k . x_j for the four streams: both are bf16 in shared memory, so that their
+// products are exact, and the tensor cores take 64 columns of all sixteen sums in two instructions where
+// the FMA pipe takes 32. Rows 0..3 of A and columns 0..3 of B are the streams at one half of the columns,
+// rows and columns 4..7 at the other; the blocks between them are not used. A lane's 8 columns are its
+// k-slots of both instructions, the same ones in A and B. Lanes 4 k + m (k < 4, m < 2) return sums j = 2m, 2m + 1.
+__device__ __forceinline__ f2 stream_dots(const uint8_t* gxp, const uint8_t* x, int d, int warp, int warps) {
+  const int lane = threadIdx.x & 31, k = (lane >> 2) & 3;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int base = warp * 64; base < d; base += warps * 64) {   // the whole warp together
+    const int c = base + (lane >> 4) * 32 + (lane & 3) * 8;
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+    if (c < d) {
+      a = *reinterpret_cast<const uint4*>(gxp + 2 * (k * d + c));
+      b = *reinterpret_cast<const uint4*>(x + 2 * (k * d + c));
+    }
+    mma_rows8(acc, a.x, a.y, b.x, b.y);
+    mma_rows8(acc, a.z, a.w, b.z, b.w);
+  }
+  return f2{acc[0] + __shfl_down_sync(0xffffffffu, acc[0], 18), acc[1] + __shfl_down_sync(0xffffffffu, acc[1], 18)};
 }
 
 // Threads of the backward's blocks: 11 consumer warps and the producer, 168 registers a thread (80 with one
@@ -644,7 +677,9 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
     norm_step_backward_staged(const NormArgs P, const Ring R) {
   constexpr int IE = 2, IG = 4 + 2 * NS;  // where gg.z, gg.x_j and gXp_k.z, gXp_k.x_j begin
   constexpr int V = NS == 4 ? 32 : 8;
-  static_assert(IG + NS + NS * NS == V, "sums");
+  constexpr bool DOTS = NS == 4 && !CK;   // gXp_k . x_j by stream_dots
+  constexpr int VF = DOTS ? 16 : V;       // sums taken by the threads
+  static_assert(IG + NS + NS * NS == V && (!DOTS || IG + NS == VF), "sums");
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ Barriers B;
   __shared__ float scratch1[SMAX_WARPS], scratch2[2][SMAX_WARPS * V], scratch3[SMAX_WARPS * 2];
@@ -760,9 +795,9 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
       C4 yh[UN];
       float tot;
       {
-        float v[V];
+        float v[VF];
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.f;
+        for (int i = 0; i < VF; ++i) v[i] = 0.f;
         auto dot = [&](int i, f2 a, f2 b) { v[i] = fmaf(a.x, b.x, fmaf(a.y, b.y, v[i])); };
 #pragma unroll
         for (int q = 0; q < UN; ++q) {
@@ -800,16 +835,33 @@ __global__ void __launch_bounds__(SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
               dot(IE + 1 + j, gg, xi[j]);
               dot(IE + NS + 2 + j, y, xi[j]);
               dot(IG + j, gi[j], z);
+              if constexpr (!DOTS) {
 #pragma unroll
-              for (int k = 0; k < NS; ++k) dot(IG + NS + j * NS + k, gi[k], xi[j]);
+                for (int k = 0; k < NS; ++k) dot(IG + NS + j * NS + k, gi[k], xi[j]);
+              }
             }
             yh[q].v[i] = y;
+          }
+        }
+        float* scratch = scratch2[n & 1];
+        if constexpr (DOTS) {
+          __syncwarp();   // the loop above ends early for some lanes
+          const f2 m = stream_dots(st + S.gxp, xt, P.d, threadIdx.x >> 5, warps);
+          if (lane < 16 && (lane & 3) < 2) {
+            float* o = scratch + (threadIdx.x >> 5) * V + IG + NS + 2 * (lane & 3) * NS + (lane >> 2);
+            o[0] = m.x;
+            o[NS] = m.y;
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.xempty[xp.stage]);
         xp.next(R.x);
-        tot = group_sums<V>(v, scratch2[n & 1], warps, T);
+        const float mine = warp_sums<VF>(v);
+        if (lane < VF) scratch[(threadIdx.x >> 5) * V + lane] = mine;
+        named_bar_sync(1, T);
+        tot = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < warps; ++i) tot += scratch[i * V + (lane & (V - 1))];
       }
       const float ry = inv_rms(lane_value(tot, 0), inv_d, P.eps);
       const float tau = ry * ry * ry * lane_value(tot, 1) * inv_d;

@@ -26,7 +26,7 @@ def test_checkpoint_validation(M, call):
     assert f(*p, -1, 64, None) == M.MHC_ERR_SHAPE
     assert f(*p, 4, 0, None) == M.MHC_ERR_SHAPE
     assert f(*p, 4, 60, None) == M.MHC_ERR_SHAPE
-    assert f(*p, (1 << 40) + 1, 64, None) == M.MHC_ERR_SHAPE
+    assert f(*p, (1 << 38) + 1, 64, None) == M.MHC_ERR_SHAPE
     assert f(None, None, None, 0, 64, None) == M.MHC_OK
     for i in range(3):
         q = list(p)
