@@ -233,9 +233,8 @@ size_t mhc_backward_workspace_bytes(int64_t N, int n, int d);
  *   block; an infinity or NaN becomes a NaN code, its neighbours keep their values.
  * mhc_checkpoint_load: codes, scales -> x bf16 [rows, d] = value(code) 2^(scale - 127), rounded to
  *   nearest even (exact for every block whose amax was at least 2^-116; scale code 255 gives NaN).
- * The streams X [N, n, d] are N n rows. rows x d, d rounded up to whole blocks, is at most 2^44
- * (MHC_ERR_SHAPE); rows == 0 is MHC_OK. No output may
- * overlap an input or the other output.                                                       */
+ * The streams X [N, n, d] are N n rows. rows x d, d rounded up to whole blocks, is at most 2^43
+ * (MHC_ERR_SHAPE); rows == 0 is MHC_OK. No output may overlap an input or the other output.   */
 int mhc_checkpoint_save(const void* x, void* codes, void* scales, int64_t rows, int d, void* stream);
 int mhc_checkpoint_load(const void* codes, const void* scales, void* x, int64_t rows, int d,
                         void* stream);

@@ -274,9 +274,9 @@ int backward_common(const BwdArgs& a, int n, const BwdCheckpoint* c, void* strea
   return cuda_code(c ? launch_backward_ckpt(a, *c, s) : launch_backward(a, s));
 }
 
-// Rows of a checkpoint of width d: what one grid covers (16 TB of codes).
+// Rows of a checkpoint of width d: what one grid covers (8 TB of codes).
 bool rows_ok(int64_t rows, int d) {
-  return rows >= 0 && d > 0 && d % 8 == 0 && rows <= (int64_t(1) << 44) / ((static_cast<int64_t>(d) + 31) / 32 * 32);
+  return rows >= 0 && d > 0 && d % 8 == 0 && rows <= (int64_t(1) << 43) / ((static_cast<int64_t>(d) + 31) / 32 * 32);
 }
 
 // Shape, flags, weights and parameters of a norm step (either direction).

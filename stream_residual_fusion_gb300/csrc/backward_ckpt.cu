@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
     const float* __restrict__ comb, const float* __restrict__ gain, const float* __restrict__ mixes,
     const float* __restrict__ gm, float* __restrict__ rec, __nv_bfloat16* __restrict__ planes_hm,
     __nv_bfloat16* __restrict__ planes_lo, float* __restrict__ gpre_prev, uint2* __restrict__ slot_scales,
+    uint4* __restrict__ Xp,
     int64_t scale_rows, int64_t N, int d, float norm_eps,
     int row_dest, float neg_zero) {
   constexpr int V = 16;   // |x|^2, |y_hat|^2, T, gain gy . X'_j, y_hat . X'_j
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
       if ((c & 3) == 0)   // the block's five scale codes, for the stream kernel
         slot_scales[(c / 4) * scale_rows + t] =
             make_uint2(cur.s[0] | (cur.s[1] << 8) | (cur.s[2] << 16) | (cur.s[3] << 24), cur.s[4]);
+      uint32_t xw[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         auto word = [&](uint2 w) { return (i < 2 ? w.x : w.y) >> (16 * (i & 1)); };
@@ -311,7 +313,8 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const f2 ck[4] = {cc[0][k], cc[1][k], cc[2][k], cc[3][k]};
-          xp[k] = bf2_to_f2(f2_to_bf2(hc_post_pair(ck, cu[k], x, f, nz)));
+          xw[k][i] = f2_to_bf2(hc_post_pair(ck, cu[k], x, f, nz));
+          xp[k] = bf2_to_f2(xw[k][i]);
           acc[0] = fma2(xp[k], xp[k], acc[0]);
         }
         const f2 yh = bf2_to_f2(f2_to_bf2(hc_pre_pair(cp, xp, nz)));
@@ -324,6 +327,9 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
           acc[7 + k] = fma2(yh, xp[k], acc[7 + k]);
         }
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        Xp[(t * 4 + k) * chunks + c] = make_uint4(xw[k][0], xw[k][1], xw[k][2], xw[k][3]);
       cur = nxt;
     }
     float v[V];
@@ -376,18 +382,19 @@ constexpr int SO_PHM = 0;                    // two of each, then W^T of two slo
 constexpr int SO_WHM = SO_PHM + 2 * SB_PHM;
 constexpr int SO_WLO = SO_WHM + 2 * W_HM;
 constexpr int SO_PLO = SO_WLO + 2 * W_LO;
-constexpr int SO_XP = SO_PLO + 2 * SB_PLO;   // X' of the slot, [96 x 32] bf16 of each stream
-constexpr int SO_B = SO_XP + 4 * SB_TILE;    // gXp, gy -> gX, gF
+constexpr int SO_XP = SO_PLO + 2 * SB_PLO;   // X' of two slots, [96 x 32] bf16 of each stream
+constexpr int SB_XP = 4 * SB_TILE;
+constexpr int SO_B = SO_XP + 2 * SB_XP;    // gXp, gy -> gX, gF
 constexpr int SO_C = SO_B + 2 * SB_SET;      // codes
 constexpr int SB_SCALES = SBR * 8;           // scale codes of a slot, then its 32 gains
 constexpr int SB_SIDE = SB_SCALES + 128;
 constexpr int SO_S = SO_C + 2 * SB_CODES;
 constexpr int SO_BARS = SO_S + 2 * SB_SIDE;
-constexpr int SB_NBARS = 2 * 11 + 4;
+constexpr int SB_NBARS = 2 * 13 + 2;
 constexpr int SB_SLOTS = 8;                  // slots of a work item, at most
 constexpr int SO_GAIN = SO_BARS + SB_NBARS * 8;   // ggain sums: [6 warps][slot][16 columns]
 constexpr int SO_TMEM = SO_GAIN + 6 * SB_SLOTS * 16 * 4;
-constexpr int SB_SMEM = SO_TMEM + 16 + 1024;
+constexpr int SB_SMEM = SO_TMEM + 16;
 static_assert(SB_SMEM <= 232448, "shared memory budget");
 static_assert(SB_PHM % 1024 == 0 && W_HM % 1024 == 0 && SO_PLO % 1024 == 0 && SB_PLO % 512 == 0 &&
                   SB_TILE % 512 == 0 && SB_CODE % 256 == 0 && SO_XP % 512 == 0 && SO_C % 256 == 0,
@@ -428,10 +435,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                       const __grid_constant__ CUtensorMap tm_gxp, const __grid_constant__ CUtensorMap tm_gy,
                       const __grid_constant__ CUtensorMap tm_gx, const __grid_constant__ CUtensorMap tm_gf,
                       const __grid_constant__ CUtensorMap tm_hm, const __grid_constant__ CUtensorMap tm_lo,
-                      const SbParams P) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+                      const __grid_constant__ CUtensorMap tm_xp, const SbParams P) {
+  extern __shared__ __align__(1024) uint8_t sm[];   // the block has no other shared memory before it
   uint64_t* cfull = reinterpret_cast<uint64_t*>(sm + SO_BARS);
   uint64_t* cempty = cfull + 2;
   uint64_t* bfull = cempty + 2;
@@ -443,9 +448,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
   uint64_t* pempty = pfull + 2;
   uint64_t* wfull = pempty + 2;
   uint64_t* wempty = wfull + 2;
-  uint64_t* xready = wempty + 2;
-  uint64_t* xfree = xready + 1;
-  uint64_t* gwfull = xfree + 1;
+  uint64_t* xfull = wempty + 2;
+  uint64_t* xempty = xfull + 2;
+  uint64_t* gwfull = xempty + 2;
   uint64_t* gwfree = gwfull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SO_TMEM);
 
@@ -478,9 +483,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       mbar_init(&pempty[i], 1);
       mbar_init(&wfull[i], 1);
       mbar_init(&wempty[i], 1);
+      mbar_init(&xfull[i], 1);
+      mbar_init(&xempty[i], 1 + SB_CONS);
     }
-    mbar_init(xready, SB_CONS);
-    mbar_init(xfree, 1);
     mbar_init(gwfull, 1);
     mbar_init(gwfree, SB_CONS);
     fence_mbar_init();
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
     if (lane == 0) {
       // ---------------------------------------------------------------- loads
       const uint64_t pol = policy_evict_normal(), wpol = policy_evict_last();
-      const uint32_t code_bytes = (5u * 32u + 8u) * tt + 128u, b_bytes = 5u * 64u * tt;
+      const uint32_t code_bytes = (5u * 32u + 8u) * tt + 128u, b_bytes = 5u * 64u * tt, x_bytes = 4u * 64u * tt;
       int u = 0, tn = 0;   // slots and tiles of this block so far
       for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int col0 = column(item), ns = slots(item);
@@ -535,6 +540,11 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             uint8_t* side = sm + SO_S + e * SB_SIDE;
             bulk_load_hint(side, P.scales + (static_cast<size_t>(col / 32) * P.ntiles * tt + t0), 8u * tt, &cfull[e], pol);
             bulk_load_hint(side + SB_SCALES, P.gain + col, 128, &cfull[e], wpol);
+            if (u >= 2) wait(&xempty[e], (u >> 1) - 1);
+            mbar_arrive_expect_tx(&xfull[e], x_bytes);
+            uint8_t* x = sm + SO_XP + e * SB_XP;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tma_load_3d_hint(x + k * SB_TILE, &tm_xp, &xfull[e], col, k, t0, pol);
             if (u >= 2) wait(&bempty[e], (u >> 1) - 1);
             mbar_arrive_expect_tx(&bfull[e], b_bytes);
             uint8_t* b = sm + SO_B + e * SB_SET;
@@ -622,12 +632,12 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
       auto issue = [&](const Place& nx, int u) {
         if (nx.item < items) product(nx, u + 1);
         // gW += X'^T (r g_m) of slot u
-        wait(xready, u);
+        wait(&xfull[u & 1], u >> 1);
         const bool start = cur.tile == first_tile(cur.item);
         if (start && cur.s == 0 && cur.in > 0) wait(gwfree, cur.in - 1);
         tc_fence_after();
         const int pb = cur.tn & 1;
-        const uint32_t xa = smem_u32(sm + SO_XP);
+        const uint32_t xa = smem_u32(sm + SO_XP + (u & 1) * SB_XP);
         const uint32_t phm = smem_u32(sm + SO_PHM + pb * SB_PHM), plo = smem_u32(sm + SO_PLO + pb * SB_PLO);
         const uint32_t acc = tmem + 256u + 32u * static_cast<uint32_t>(cur.s);
         const bool last = cur.s == slots(cur.item) - 1;
@@ -637,7 +647,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           umma_bf16(acc, a, sdesc_mnmajor(phm + 64 + ks * 2048, 128, 0, 1024), id_w, 1u);
           umma_bf16(acc, a, sdesc_mnmajor(phm + ks * 2048, 128, 0, 1024), id_w, 1u);
         }
-        umma_commit(xfree);
+        umma_commit(&xempty[u & 1]);
         if (last) umma_commit(&pempty[pb]);
         if (last && cur.tile == last_tile(cur.item) - 1) umma_commit(gwfull);
       };
@@ -716,7 +726,9 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           const int e = u & 1;
           uint8_t* codes = sm + SO_C + e * SB_CODES;
           uint8_t* bt = sm + SO_B + e * SB_SET;
+          const uint8_t* xt = sm + SO_XP + e * SB_XP;
           wait(&cfull[e], u >> 1);
+          wait(&xfull[e], u >> 1);
           wait(&bfull[e], u >> 1);
           wait(&dready[e], u >> 1);
           tc_fence_after();
@@ -737,11 +749,13 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
             const uint2 fc = *reinterpret_cast<const uint2*>(codes + 4 * SB_CODE + code_off + 8 * q);
             float gsum[8];   // ggain's terms of this token
             // gXp and gy, then gX and gF in their place
-            uint32_t ga[4][4], ya[4], xw[4][4];
+            uint32_t ga[4][4], ya[4], xw[4][4];   // xw: X'
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint4 g = *reinterpret_cast<const uint4*>(bt + k * SB_TILE + row_off(q));
               ga[k][0] = g.x; ga[k][1] = g.y; ga[k][2] = g.z; ga[k][3] = g.w;
+              const uint4 v = *reinterpret_cast<const uint4*>(xt + k * SB_TILE + row_off(q));
+              xw[k][0] = v.x; xw[k][1] = v.y; xw[k][2] = v.z; xw[k][3] = v.w;
             }
             {
               const uint4 y = *reinterpret_cast<const uint4*>(bt + 4 * SB_TILE + row_off(q));
@@ -766,11 +780,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = decode2(word(xc[j]), f2{sx[j], sx[j]});
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const f2 ck[4] = {cc[0][k], cc[1][k], cc[2][k], cc[3][k]};
-                  xw[k][w] = f2_to_bf2(hc_post_pair(ck, cu[k], x, f, nz));
-                  xp[k] = bf2_to_f2(xw[k][w]);
-                }
+                for (int k = 0; k < 4; ++k) xp[k] = bf2_to_f2(xw[k][w]);
                 const f2 yh = bf2_to_f2(f2_to_bf2(hc_pre_pair(cpp, xp, nz)));
                 const f2 ryg = mul2(r_y2, bf2_to_f2(ya[w]));
                 const f2 gyh = fma2(ryg, gn[i], mul2(tau2, yh));
@@ -803,17 +813,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
                 ya[w] = f2_to_bf2(vf);
               }
             }
-            if (q == 0 && u > 0) wait(xfree, u - 1);   // gW has read the last slot's X'
-            {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                *reinterpret_cast<uint4*>(sm + SO_XP + k * SB_TILE + row_off(q)) =
-                    make_uint4(xw[k][0], xw[k][1], xw[k][2], xw[k][3]);
-                *reinterpret_cast<uint4*>(bt + k * SB_TILE + row_off(q)) =
-                    make_uint4(ga[k][0], ga[k][1], ga[k][2], ga[k][3]);
-              }
-              *reinterpret_cast<uint4*>(bt + 4 * SB_TILE + row_off(q)) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
-            }
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(bt + k * SB_TILE + row_off(q)) = make_uint4(ga[k][0], ga[k][1], ga[k][2], ga[k][3]);
+            *reinterpret_cast<uint4*>(bt + 4 * SB_TILE + row_off(q)) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
             const float gt = warp_sums<8>(gsum);   // lane l: column l % 8
             if (lane < 8) gain_sum[16 * s + 8 * q] += gt;
           }
@@ -822,7 +825,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&dfree[e]);
-            mbar_arrive(xready);
+            mbar_arrive(&xempty[e]);
             mbar_arrive(&gready[e]);
             if (s < ns - 1) mbar_arrive(&cempty[e]);
           }
@@ -976,7 +979,7 @@ __global__ void __launch_bounds__(256) ckb_reduce_kernel(const ReduceParams P) {
 
 // Byte offsets of the workspace's parts and the work split.
 struct Plan {
-  size_t wt, gm, rec, hm, lo, scales, mix, gain, w, t, bytes;
+  size_t wt, gm, rec, hm, lo, xp, scales, mix, gain, w, t, bytes;
   int tt, ntiles, per, ranges, spb, nblocks;   // stream kernel
   int mix_blocks;
 };
@@ -1026,6 +1029,7 @@ Plan search_plan(int64_t N, int d, int sms) {
   p.rec = part(n * 16);
   p.hm = part(n * 128);
   p.lo = part(n * 64);
+  p.xp = part(n * 8 * d);
   p.scales = part(static_cast<size_t>(d / 32) * p.ntiles * p.tt * 8);
   p.mix = part(static_cast<size_t>(p.mix_blocks) * 128);
   p.gain = part(static_cast<size_t>(p.ranges) * 3 * d * 4);
@@ -1097,7 +1101,7 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
       kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 2 * static_cast<int64_t>(sms))), TOKEN_WARPS * 32, 0, stream>>>(
           in, static_cast<const uint4*>(a.gy), a.pre_prev, a.post_prev, a.comb_prev, a.gain, a.mixes, wsf(p.gm),
           wsf(p.rec), reinterpret_cast<__nv_bfloat16*>(ws + p.hm), reinterpret_cast<__nv_bfloat16*>(ws + p.lo),
-          a.gpre_prev, reinterpret_cast<uint2*>(ws + p.scales), static_cast<int64_t>(p.ntiles) * p.tt, N, d, a.norm_eps,
+          a.gpre_prev, reinterpret_cast<uint2*>(ws + p.scales), reinterpret_cast<uint4*>(ws + p.xp), static_cast<int64_t>(p.ntiles) * p.tt, N, d, a.norm_eps,
           row_dest, -0.0f);
       return cudaGetLastError();
     };
@@ -1108,12 +1112,13 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
   }
   {
     const uint32_t tt = static_cast<uint32_t>(p.tt);
-    CUtensorMap tx, tf, tgxp, tgy, tgx, tgf, thm, tlo;
+    CUtensorMap tx, tf, tgxp, tgy, tgx, tgf, thm, tlo, txp;
     if (!code_map(&tx, ck.X_codes, N, d, 4, tt) || !code_map(&tf, ck.F_codes, N, d, 1, tt) ||
         !bmap_streams(&tgxp, a.gXp, N, d, tt) || !bmap_rows(&tgy, a.gy, N, d, 32, tt, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !bmap_streams(&tgx, a.gX, N, d, tt) || !bmap_rows(&tgf, a.gF, N, d, 32, tt, CU_TENSOR_MAP_SWIZZLE_64B) ||
         !bmap_rows(&thm, ws + p.hm, N, 64, 64, tt, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !bmap_rows(&tlo, ws + p.lo, N, 32, 32, tt, CU_TENSOR_MAP_SWIZZLE_64B))
+        !bmap_rows(&tlo, ws + p.lo, N, 32, 32, tt, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !bmap_streams(&txp, ws + p.xp, N, d, tt))
       return cudaErrorInvalidValue;
     SbParams P{};
     P.pre = a.pre_prev;
@@ -1140,7 +1145,7 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
     e = allow_shared_memory(reinterpret_cast<const void*>(ckb_stream_kernel));
     if (e != cudaSuccess) return e;
     const int items = p.nblocks * p.ranges;
-    ckb_stream_kernel<<<std::min(items, sms), SB_THREADS, SB_SMEM, stream>>>(tx, tf, tgxp, tgy, tgx, tgf, thm, tlo, P);
+    ckb_stream_kernel<<<std::min(items, sms), SB_THREADS, SB_SMEM, stream>>>(tx, tf, tgxp, tgy, tgx, tgf, thm, tlo, txp, P);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
