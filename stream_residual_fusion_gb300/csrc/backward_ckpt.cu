@@ -286,12 +286,21 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
       o.s[4] = __ldg(in.Fs + t * blocks + c / 4);
       o.gy = __ldg(gy + t * chunks + c);
     };
-    // the next chunk's loads are issued before this one's arithmetic
-    Raw cur, nxt;
+    Raw cur;
     int c = (warp % WPT) * 32 + lane;
-    if (c < chunks) fetch(c, cur);
     for (; c < chunks; c += 32 * WPT) {
-      if (c + 32 * WPT < chunks) fetch(c + 32 * WPT, nxt);
+      fetch(c, cur);
+      // the lines of the next chunk, or of the next token's first one: 128 registers do not hold a chunk
+      // ahead, and 16 warps alone do not cover the latency (1,840 us without, 1,752 with it at 32,768 tokens)
+      const bool more = c + 32 * WPT < chunks;
+      const int pc = more ? c + 32 * WPT : (warp % WPT) * 32 + lane;
+      const int64_t pt = more ? t : t + step;
+      if (pt < N && pc < chunks) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) prefetch_l1(in.X + (pt * 4 + k) * chunks + pc);
+        prefetch_l1(in.F + pt * chunks + pc);
+        prefetch_l1(gy + pt * chunks + pc);
+      }
       const float4 g0 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * c);
       const float4 g1 = __ldg(reinterpret_cast<const float4*>(gain) + 2 * c + 1);
       const f2 ga[4] = {f2{g0.x, g0.y}, f2{g0.z, g0.w}, f2{g1.x, g1.y}, f2{g1.z, g1.w}};
@@ -330,7 +339,6 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         Xp[(t * 4 + k) * chunks + c] = make_uint4(xw[k][0], xw[k][1], xw[k][2], xw[k][3]);
-      cur = nxt;
     }
     float v[V];
 #pragma unroll
