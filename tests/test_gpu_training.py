@@ -288,6 +288,12 @@ NORM_CASES = [
     (40, 1, 5120, "linear", True, True, True, False),
     (2, 1, 32768, "sigmoid", True, False, False, False),
     (1, 1, 16, "none", False, True, False, True),
+    (77, 4, 64, "sigmoid", True, True, True, False),
+    (260, 4, 248, "none", True, True, False, True),
+    (19, 4, 1032, "sigmoid", True, True, False, False),
+    (130, 1, 200, "linear", True, True, True, False),
+    (600, 1, 1024, "sigmoid", False, False, False, False),
+    (6, 4, 7168, "none", False, True, True, False),
 ]
 
 
