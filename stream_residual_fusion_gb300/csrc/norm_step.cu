@@ -922,12 +922,13 @@ __device__ __forceinline__ void put_gains(float* row, int d, const Span4& sp, co
   }
 }
 
-// Threads of the backward's blocks: 11 consumer warps and the producer, 168 registers a thread (fewer
-// with few features, for more blocks a multiprocessor: 128 with four bf16 streams, 80 with one).
+// Threads of the backward's blocks: 11 consumer warps and the producer, at 168 registers a thread. BOUND caps the
+// registers further where that lets a multiprocessor hold more blocks of few threads: 512 for 128 registers,
+// 768 for 80.
 constexpr int SBACK_THREADS = 384;
 
-template <int NS, bool CK, int UN>
-__global__ void __launch_bounds__(NS == 4 && !CK && UN == 2 ? 512 : SBACK_THREADS, NS == 1 && UN == 2 ? 2 : 1)
+template <int NS, bool CK, int UN, int BOUND = SBACK_THREADS>
+__global__ void __launch_bounds__(BOUND, 1)
     norm_step_backward_staged(const NormArgs P, const Ring R) {
   using S = Sums<NS, CK>;
   extern __shared__ __align__(128) uint8_t sm[];
@@ -1326,14 +1327,27 @@ cudaError_t backward_of(const NormArgs& a, const DeviceInfo& dev, int* rows, cud
   if (!CK || a.d % 16 == 0) {
     const Stage stage = stage_of<NS, CK, true>(a.d);
     const int most = SBACK_THREADS - 32;
-    cudaError_t e;
-    if (const int t = staged_threads(a.d / 4, 2, most))
-      e = launch_staged(norm_step_backward_staged<NS, CK, 2>, a, t, stage, dev, NORM_BACK_BLOCKS, rows, stream);
-    else if (const int t4 = staged_threads(a.d / 4, 4, most))
-      e = launch_staged(norm_step_backward_staged<NS, CK, 4>, a, t4, stage, dev, NORM_BACK_BLOCKS, rows, stream);
-    else
-      e = launch_staged(norm_step_backward_staged<NS, CK, 6>, a, staged_threads(a.d / 4, 6, most), stage, dev,
-                        NORM_BACK_BLOCKS, rows, stream);
+    const int t2 = staged_threads(a.d / 4, 2, most), t4 = staged_threads(a.d / 4, 4, most);
+    auto run = [&](auto kernel, int threads) {
+      return launch_staged(kernel, a, threads, stage, dev, NORM_BACK_BLOCKS, rows, stream);
+    };
+    // Two units a thread where that fits (four streams, 128 registers: 301 us at 20,480 x 4 x 1,024, 398 with
+    // 168). At middling widths more units make blocks of fewer threads, more of which fit: four units of one
+    // stream (389 us against 455 at 40,960 x 2,048), three of four streams (300 against 418 at 10,240 x 4 x 2,048).
+    auto middling = [&]() {
+      if constexpr (NS == 1) {
+        if (t4 >= 96 && t4 <= 160) return run(norm_step_backward_staged<NS, CK, 4, 512>, t4);
+      } else if constexpr (!CK) {
+        const int t3 = staged_threads(a.d / 4, 3, most);
+        if (t3 >= 128 && t3 <= 192) return run(norm_step_backward_staged<NS, CK, 3, 512>, t3);
+      }
+      return cudaSuccess;
+    };
+    cudaError_t e = middling();
+    if (e != cudaSuccess || *rows > 0) return e;
+    if (t2 > 0) e = run(norm_step_backward_staged<NS, CK, 2, NS == 1 ? 768 : CK ? SBACK_THREADS : 512>, t2);
+    else if (t4 > 0) e = run(norm_step_backward_staged<NS, CK, 4>, t4);
+    else e = run(norm_step_backward_staged<NS, CK, 6>, staged_threads(a.d / 4, 6, most));
     if (e != cudaSuccess || *rows > 0) return e;
   }
   *rows = static_cast<int>(std::min<int64_t>(a.N, 2 * static_cast<int64_t>(dev.sms)));
