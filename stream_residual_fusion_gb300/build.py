@@ -22,7 +22,7 @@ LIB_CHECKED = os.path.join(PKG, "libmhc_checked.so")
 SOURCES = ["fused.cu", "cluster.cu", "small.cu", "abi.cu", "host_pipeline.cu", "backward.cu",
            "backward_ckpt.cu", "checkpoint.cu", "norm_step.cu"]
 HEADERS = ["ptx.cuh", "mix_math.cuh", "hc_arith.cuh", "internal.h", "layout.cuh", "mx8.cuh", "bwd_parts.cuh",
-           "block_sums.cuh"]
+           "block_sums.cuh", "chain.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fmad=false: a separate float32 multiply and add must stay two roundings (hc_post and hc_pre

@@ -27,6 +27,7 @@
 
 #include "block_sums.cuh"
 #include "bwd_parts.cuh"
+#include "chain.cuh"
 #include "hc_arith.cuh"
 #include "internal.h"
 #include "layout.cuh"
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(PREP_THREADS) ckb_prep_kernel(
     const float* __restrict__ gcomb, const float* __restrict__ scale, const float* __restrict__ base,
     const float* __restrict__ W, float* __restrict__ gm, float* __restrict__ part, uint8_t* __restrict__ wT,
     int64_t N, int d, int iters, float eps, int mix_blocks, int every) {
+  open_next();
   extern __shared__ float4 kept[];   // [step / every][thread]
   __shared__ float red[PREP_THREADS / 32][MIXN + 3];
   if (static_cast<int>(blockIdx.x) >= mix_blocks) {
@@ -224,12 +226,12 @@ struct CkIn {
   const uint8_t* Fs;
 };
 
-// WPT warps a token: one where there are enough tokens to fill the device, else the whole block.
+// WPT warps a token: as many, up to the whole block, as leave no warp of the device without one.
 template <int WPT>
 __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
     const CkIn in, const uint4* __restrict__ gy, const float* __restrict__ pre, const float* __restrict__ post,
     const float* __restrict__ comb, const float* __restrict__ gain, const float* __restrict__ mixes,
-    const float* __restrict__ gm, float* __restrict__ rec, __nv_bfloat16* __restrict__ planes_hm,
+    const float* gm, float* __restrict__ rec, __nv_bfloat16* __restrict__ planes_hm,
     __nv_bfloat16* __restrict__ planes_lo, float* __restrict__ gpre_prev, uint2* __restrict__ slot_scales,
     uint4* __restrict__ Xp,
     int64_t scale_rows, int64_t N, int d, float norm_eps,
@@ -244,11 +246,8 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
   const int64_t step = static_cast<int64_t>(gridDim.x) * TPB;
   int n = 0;
   for (int64_t t = blockIdx.x * static_cast<int64_t>(TPB) + warp / WPT; t < N; t += step, ++n) {
-    float gmi = 0.f, mi = 0.f;
-    if (lane < MIXN) {
-      gmi = __ldg(gm + t * MIXN + lane);
-      mi = __ldg(mixes + t * MIXN + lane);
-    }
+    const float mi = lane < MIXN ? __ldg(mixes + t * MIXN + lane) : 0.f;
+    float gmi = n > 0 && lane < MIXN ? gm[t * MIXN + lane] : 0.f;   // there once the first token is done
     f2 cc[4][4], cu[4], cp[4];
     {
       const float4 u4 = __ldg(reinterpret_cast<const float4*>(post) + t), p4 = __ldg(reinterpret_cast<const float4*>(pre) + t);
@@ -344,8 +343,18 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = i < 11 ? acc[i].x + acc[i].y : 0.f;
     float tot;   // lane l: the token's total of value l % 16
-    if constexpr (WPT == 1) tot = warp_sums<V>(v);
-    else tot = group_sums<V>(v, scratch[n & 1], TOKEN_WARPS, TOKEN_WARPS * 32);
+    tot = warp_sums<V>(v);
+    if constexpr (WPT > 1) {   // the token's warps together, at a barrier of their own
+      if (lane < V) scratch[n & 1][warp * V + lane] = tot;
+      named_bar_sync(1 + warp / WPT, WPT * 32);
+      tot = 0.f;
+#pragma unroll
+      for (int i = 0; i < WPT; ++i) tot += scratch[n & 1][(warp / WPT * WPT + i) * V + (lane & (V - 1))];
+    }
+    if (n == 0) {
+      wait_previous();
+      if (lane < MIXN) gmi = gm[t * MIXN + lane];
+    }
     if (warp % WPT == 0) {
       const float r = __frsqrt_rn(__fdiv_rn(lane_value(tot, 0), fk) + norm_eps);
       const float ry = __frsqrt_rn(__fdiv_rn(lane_value(tot, 1), fd) + norm_eps);
@@ -1105,17 +1114,20 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
   {
     const CkIn in{static_cast<const uint2*>(ck.X_codes), static_cast<const uint8_t*>(ck.X_scale),
                   static_cast<const uint2*>(ck.F_codes), static_cast<const uint8_t*>(ck.F_scale)};
-    auto run = [&](auto kernel, int64_t blocks) {
-      kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 2 * static_cast<int64_t>(sms))), TOKEN_WARPS * 32, 0, stream>>>(
-          in, static_cast<const uint4*>(a.gy), a.pre_prev, a.post_prev, a.comb_prev, a.gain, a.mixes, wsf(p.gm),
-          wsf(p.rec), reinterpret_cast<__nv_bfloat16*>(ws + p.hm), reinterpret_cast<__nv_bfloat16*>(ws + p.lo),
-          a.gpre_prev, reinterpret_cast<uint2*>(ws + p.scales), reinterpret_cast<uint4*>(ws + p.xp), static_cast<int64_t>(p.ntiles) * p.tt, N, d, a.norm_eps,
-          row_dest, -0.0f);
-      return cudaGetLastError();
+    const int64_t warps = 2 * static_cast<int64_t>(sms) * TOKEN_WARPS;   // the device holds
+    auto run = [&](auto kernel, int wpt) {
+      const int64_t blocks = (N * wpt + TOKEN_WARPS - 1) / TOKEN_WARPS;
+      // Early only while each warp has one token: blocks that start beside the first kernel's keep the small L1 that
+      // its shared memory left them, and walk all their tokens with it (32,768 tokens: 1,820 us against 1,758).
+      return launch_behind(N * wpt <= warps, kernel, static_cast<unsigned>(std::min<int64_t>(blocks, 2 * static_cast<int64_t>(sms))),
+                           TOKEN_WARPS * 32, 0, stream, in, static_cast<const uint4*>(a.gy), a.pre_prev, a.post_prev,
+                           a.comb_prev, a.gain, a.mixes, wsf(p.gm), wsf(p.rec),
+                           reinterpret_cast<__nv_bfloat16*>(ws + p.hm), reinterpret_cast<__nv_bfloat16*>(ws + p.lo),
+                           a.gpre_prev, reinterpret_cast<uint2*>(ws + p.scales), reinterpret_cast<uint4*>(ws + p.xp),
+                           static_cast<int64_t>(p.ntiles) * p.tt, N, d, a.norm_eps, row_dest, -0.0f);
     };
-    // a warp a token once every warp the device holds (two blocks a multiprocessor) has one
-    e = N >= 2 * static_cast<int64_t>(sms) * TOKEN_WARPS ? run(ckb_token_kernel<1>, (N + TOKEN_WARPS - 1) / TOKEN_WARPS)
-                                                         : run(ckb_token_kernel<TOKEN_WARPS>, N);
+    e = 2 * N > warps ? run(ckb_token_kernel<1>, 1) : 4 * N > warps ? run(ckb_token_kernel<2>, 2)
+      : 8 * N > warps ? run(ckb_token_kernel<4>, 4) : run(ckb_token_kernel<8>, 8);
     if (e != cudaSuccess) return e;
   }
   {
@@ -1153,6 +1165,7 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
     e = allow_shared_memory(reinterpret_cast<const void*>(ckb_stream_kernel));
     if (e != cudaSuccess) return e;
     const int items = p.nblocks * p.ranges;
+    // (started early, like the kernel before, it took 40 us more at 32,768 tokens and no less at few)
     ckb_stream_kernel<<<std::min(items, sms), SB_THREADS, SB_SMEM, stream>>>(tx, tf, tgxp, tgy, tgx, tgf, thm, tlo, txp, P);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

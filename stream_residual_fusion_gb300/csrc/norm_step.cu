@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "block_sums.cuh"
+#include "chain.cuh"
 #include "internal.h"
 #include "mx8.cuh"
 
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(NT) norm_step_kernel(const NormArgs P) {
 // parameter gradients gather in the block's own row of the workspace without atomics.
 template <int NS, bool CK>
 __global__ void __launch_bounds__(NT) norm_step_backward_kernel(const NormArgs P) {
+  open_next();
   constexpr int NSUM = 1 + 2 * NS + NS * NS;
   extern __shared__ float q_s[];
   __shared__ float scratch[NW * NSUM];
@@ -930,6 +932,7 @@ constexpr int SBACK_THREADS = 384;
 template <int NS, bool CK, int UN, int BOUND = SBACK_THREADS>
 __global__ void __launch_bounds__(BOUND, 1)
     norm_step_backward_staged(const NormArgs P, const Ring R) {
+  open_next();
   using S = Sums<NS, CK>;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ Barriers B;
@@ -1131,6 +1134,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, NS == 4 ? 3 : 4) norm_step_row
 // NS streams, UN units of 4 features a lane. Each block adds its warps' sums in their order and writes one row.
 template <int NS, bool CK, int UN>
 __global__ void __launch_bounds__(ROW_WARPS * 32, NS == 4 ? 3 : 4) norm_step_backward_rows(const NormArgs P) {
+  open_next();
   using S = Sums<NS, CK>;
   __shared__ __align__(16) float red[ROW_WARPS][2 * 128 * UN + 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1194,6 +1198,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, NS == 4 ? 3 : 4) norm_step_bac
 // Sums of the blocks' partial rows, in the blocks' order: 32 columns a block, 8 threads a column.
 __global__ void __launch_bounds__(256) norm_reduce_kernel(const NormArgs P, int rows) {
   __shared__ float red[8][33];
+  wait_previous();
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   const int cols = norm_partial_floats(P.d);
@@ -1378,8 +1383,8 @@ cudaError_t launch_norm_step_backward(const NormArgs& args, cudaStream_t stream)
   const cudaError_t e = a.n == 1 ? (ck ? backward_of<1, true>(a, dev, &rows, stream) : backward_of<1, false>(a, dev, &rows, stream))
                                  : (ck ? backward_of<4, true>(a, dev, &rows, stream) : backward_of<4, false>(a, dev, &rows, stream));
   if (e != cudaSuccess) return e;
-  norm_reduce_kernel<<<(norm_partial_floats(a.d) + 31) / 32, 256, 0, stream>>>(a, rows);
-  return cudaGetLastError();
+  return launch_behind(true, norm_reduce_kernel, static_cast<unsigned>((norm_partial_floats(a.d) + 31) / 32), 256, 0, stream,
+                       a, rows);
 }
 
 }  // namespace mhc
