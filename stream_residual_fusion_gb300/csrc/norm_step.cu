@@ -491,8 +491,8 @@ __device__ __forceinline__ void gate_gain(const NormArgs& P, uint4 gate, int c, 
 
 __device__ __forceinline__ float inv_rms(float sum, float inv_d, float eps) { return rsqrtf(fmaf(sum, inv_d, eps)); }
 
-template <int NS, int CH>
-__global__ void __launch_bounds__((SMAX_WARPS + 1) * 32, 1) norm_step_staged(const NormArgs P, Ring R) {
+template <int NS, int CH, int BOUND = (SMAX_WARPS + 1) * 32>
+__global__ void __launch_bounds__(BOUND, 1) norm_step_staged(const NormArgs P, Ring R) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ Barriers B;
   __shared__ float scratch[2][SMAX_WARPS * 2];
@@ -1308,12 +1308,14 @@ cudaError_t forward_of(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st
   const int most = SMAX_WARPS * 32;
   int ran = 0;
   cudaError_t e;
-  if (const int t = staged_threads(a.d / 8, 1, most))
-    e = launch_staged(norm_step_staged<NS, 1>, a, t, stage, dev, 8, &ran, stream);
-  else if (const int t2 = staged_threads(a.d / 8, 2, most))
-    e = launch_staged(norm_step_staged<NS, 2>, a, t2, stage, dev, 8, &ran, stream);
-  else
-    e = launch_staged(norm_step_staged<NS, 4>, a, staged_threads(a.d / 8, 4, most), stage, dev, 8, &ran, stream);
+  auto run = [&](auto kernel, int threads) { return launch_staged(kernel, a, threads, stage, dev, 8, &ran, stream); };
+  const int t1 = staged_threads(a.d / 8, 1, most), t2 = staged_threads(a.d / 8, 2, most);
+  // one stream: two chunks a thread and 80 registers, for more and smaller blocks a multiprocessor
+  // (2,048 features: 203 -> 185 us at 40,960 tokens)
+  constexpr int kBound = NS == 1 ? 768 : (SMAX_WARPS + 1) * 32;
+  if (NS == 4 && t1 > 0) e = run(norm_step_staged<4, 1>, t1);
+  else if (t2 > 0) e = run(norm_step_staged<NS, 2, kBound>, t2);
+  else e = run(norm_step_staged<NS, 4>, staged_threads(a.d / 8, 4, most));
   if (e != cudaSuccess || ran > 0) return e;
   return launch_rows(norm_step_kernel<NS>, a, std::min<int64_t>(a.N, static_cast<int64_t>(dev.sms) * 8), stream);
 }
