@@ -1,23 +1,33 @@
 // backward_ckpt.cu -- gradients of the single-pass mHC step from 8-bit checkpoints of its inputs.
 //
 // The formulas are those of backward.cu at X^, F^ (the decoded checkpoints), X' = bf16(hc_post(X^, F^)),
-// y_hat = bf16(hc_pre(X')) and the forward's mix numbers m. A pass over a token reads 5.16 d bytes of
-// codes and scales where backward.cu reads 8 d of X' or 10 d of X and F.
+// y_hat = bf16(hc_pre(X')) and the forward's mix numbers m. The call reads 5.16 d bytes of codes and
+// scales a token where backward.cu reads 10 d of X and F.
 //
 // Four launches on the caller's stream:
 //   ckb_prep_kernel    the split's and Sinkhorn's derivatives (g_m), four lanes a token, one row of the
 //                      4 x 4 matrix each; beside them, in blocks of their own, the bf16 planes of W^T.
-//   ckb_token_kernel   one warp or one block a token: the sums over its width that give r, r_y, tau, c1 and gp, the
-//                      three bf16 planes of r g_m; and the scale codes once more, slot by slot.
+//   ckb_token_kernel   one warp or one block a token: X' (to the workspace, bf16), the sums over its width
+//                      that give r, r_y, tau, c1 and gp, the three bf16 planes of r g_m; and the scale
+//                      codes once more, slot by slot.
 //   ckb_stream_kernel  work items of (up to 256 columns of every stream, a range of token tiles): gX, gF, ggain
-//                      and gW, for which X' never leaves the SM (below).
+//                      and gW.
 //   ckb_reduce_kernel  sums of partials in a fixed order: gW, ggain, g_base, g_scale, and gu, gC of every
 //                      token over the column blocks.
 //
 // Why the stream kernel owns columns and walks tokens: the gW accumulators of its columns stay in TMEM over
-// the range, X' feeds their tensor-core product from shared memory right after it was formed (backward.cu
-// reads X' and gy a second time for that), and a few tokens already give many SMs work. The price is gu
-// and gC in as many parts as there are column blocks, 80 bytes a token and block written and read again.
+// the range, the X' that the elementwise part reads is the tensor cores' operand too, and a few tokens
+// already give many SMs work. The price is gu and gC in as many parts as there are column blocks, 80 bytes
+// a token and block written and read again.
+//
+// X' goes through the workspace (8 d bytes a token each way) although the codes would give it again: with
+// hc_post in both kernels the stream kernel was bound by instructions, 2,119 us in all at 32,768 x 5,120
+// against 1,859 with X' stored.
+//
+// Measured at 9,728 x 5,120: prep 23 us, token 171 us (0.74 GB, 4.3 TB/s, FMA pipe 59% busy), stream 358 us
+// (1.68 GB, 4.7 TB/s, FMA 38%, tensor 18%), reduce 12 us; the call at 32,768 x 5,120 1,830 us, at
+// 1,333 x 2,560 68 us, at 8 x 5,120 43 us (four kernels one after the other, 20 Sinkhorn rounds there and back
+// in the first).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -377,11 +387,11 @@ __global__ void __launch_bounds__(TOKEN_WARPS * 32, 2) ckb_token_kernel(
 // ---------------------------------------------------------------------------------------------
 // ckb_stream_kernel: per work item, W^T (r g_m) and gW on the tensor cores around the elementwise
 // gradients. A tile is up to 96 tokens; a slot is 32 columns of every stream of a tile.
-//   warp 3, lane 0   TMA loads, two slots ahead: codes, gXp and gy, W^T; and the tile's planes of r g_m.
+//   warp 3, lane 0   TMA loads, two slots ahead: codes, X', gXp and gy, W^T; and the tile's planes of r g_m.
 //   warp 3, lane 1   TMA stores of gX, gF, which were written over gXp and gy.
 //   warp 7, lane 0   the MMAs: D = A W^T^T for the next slot (A = the planes [tokens x 24] of r g_m; the six
 //                    products of planes of the three largest orders), then gW += X'^T A of this slot, its three
-//                    planes into one accumulator, once the consumers have laid X' down.
+//                    planes into one accumulator.
 //   the others       two threads a token, 16 columns of the slot each, and ggain of those columns.
 // Eight warps leave each thread 255 registers, which its token's weights (as pairs), sums and operands take:
 // with ten (168 registers) what was spilled missed the little L1 beside 220 KB of shared memory, and a slot
@@ -401,7 +411,7 @@ constexpr int SO_WLO = SO_WHM + 2 * W_HM;
 constexpr int SO_PLO = SO_WLO + 2 * W_LO;
 constexpr int SO_XP = SO_PLO + 2 * SB_PLO;   // X' of two slots, [96 x 32] bf16 of each stream
 constexpr int SB_XP = 4 * SB_TILE;
-constexpr int SO_B = SO_XP + 2 * SB_XP;    // gXp, gy -> gX, gF
+constexpr int SO_B = SO_XP + 2 * SB_XP;      // gXp, gy -> gX, gF
 constexpr int SO_C = SO_B + 2 * SB_SET;      // codes
 constexpr int SB_SCALES = SBR * 8;           // scale codes of a slot, then its 32 gains
 constexpr int SB_SIDE = SB_SCALES + 128;
@@ -409,6 +419,11 @@ constexpr int SO_S = SO_C + 2 * SB_CODES;
 constexpr int SO_BARS = SO_S + 2 * SB_SIDE;
 constexpr int SB_NBARS = 2 * 13 + 2;
 constexpr int SB_SLOTS = 8;                  // slots of a work item, at most
+// Tiles of a work item, at most. The tensor cores cut each sum that they add to an accumulator down to 24 bits
+// toward zero, three times for 16 tokens: gW is off by 3e-7 of itself for each tile, in one direction. Items of
+// 24 tiles gave 8e-6 (16,000 x 5,120). Three leave it under 1e-6, about what a float32 matrix product has, for
+// 2% of the time (the partial sums of more items).
+constexpr int SB_RANGE = 3;
 constexpr int SO_GAIN = SO_BARS + SB_NBARS * 8;   // ggain sums: [6 warps][slot][16 columns]
 constexpr int SO_TMEM = SO_GAIN + 6 * SB_SLOTS * 16 * 4;
 constexpr int SB_SMEM = SO_TMEM + 16;
@@ -658,12 +673,14 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
         const uint32_t phm = smem_u32(sm + SO_PHM + pb * SB_PHM), plo = smem_u32(sm + SO_PLO + pb * SB_PLO);
         const uint32_t acc = tmem + 256u + 32u * static_cast<uint32_t>(cur.s);
         const bool last = cur.s == slots(cur.item) - 1;
-        for (int ks = 0; ks < tt / 16; ++ks) {
-          const uint64_t a = sdesc_mnmajor(xa + ks * 1024, 64, SB_TILE, 512);
-          umma_bf16(acc, a, sdesc_mnmajor(plo + ks * 1024, 64, 0, 512), id_w, (start && ks == 0) ? 0u : 1u);
-          umma_bf16(acc, a, sdesc_mnmajor(phm + 64 + ks * 2048, 128, 0, 1024), id_w, 1u);
-          umma_bf16(acc, a, sdesc_mnmajor(phm + ks * 2048, 128, 0, 1024), id_w, 1u);
-        }
+        auto x_of = [&](int ks) { return sdesc_mnmajor(xa + ks * 1024, 64, SB_TILE, 512); };
+        // the smallest planes first: what they add is cut off less while the sum is small
+        for (int ks = 0; ks < tt / 16; ++ks)
+          umma_bf16(acc, x_of(ks), sdesc_mnmajor(plo + ks * 1024, 64, 0, 512), id_w, (start && ks == 0) ? 0u : 1u);
+        for (int ks = 0; ks < tt / 16; ++ks)
+          umma_bf16(acc, x_of(ks), sdesc_mnmajor(phm + 64 + ks * 2048, 128, 0, 1024), id_w, 1u);
+        for (int ks = 0; ks < tt / 16; ++ks)
+          umma_bf16(acc, x_of(ks), sdesc_mnmajor(phm + ks * 2048, 128, 0, 1024), id_w, 1u);
         umma_commit(&xempty[u & 1]);
         if (last) umma_commit(&pempty[pb]);
         if (last && cur.tile == last_tile(cur.item) - 1) umma_commit(gwfull);
@@ -914,9 +931,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------------------------
-// ckb_reduce_kernel: float4 sums of partials in their order. Blocks [0, gw) sum gW over the ranges,
-// [gw, gw + gg) ggain over the ranges and lane quarters (8 threads an output), [.., + gt) gu and gC of the tokens
-// over the column blocks, and the last one g_base and g_scale.
+// ckb_reduce_kernel: float4 sums of partials in a fixed order. Blocks [0, gw) sum gW over the ranges,
+// [gw, gw + gg) ggain over the ranges and lane quarters (both 8 threads an output, gW of few ranges one), [.., + gt) gu and gC of the
+// tokens over the column blocks, and the last one g_base and g_scale (in 64 bits: few outputs, many terms that
+// cancel).
 struct ReduceParams {
   const float* part_w;
   const float* part_gain;
@@ -933,6 +951,7 @@ struct ReduceParams {
   int ranges, gain_rows, mix_blocks, col_blocks;
   int gw, gg;
   int64_t gt;
+  bool few;   // ranges: fewer than a block's warps
 };
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
@@ -941,51 +960,55 @@ __global__ void __launch_bounds__(256) ckb_reduce_kernel(const ReduceParams P) {
   __shared__ float4 red[8][32];
   const int64_t blk = blockIdx.x;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (blk < P.gw) {
-    const int64_t n4 = static_cast<int64_t>(MIXN) * P.d, i = blk * 256 + threadIdx.x;
-    if (i >= n4) return;
+  // Sum i of n4, whose terms are n4 apart: a thread alone, or the same lane of each warp together.
+  auto alone = [&](const float* part, int64_t rows, int64_t n4, int64_t i) {
     float4 v = zero;
-#pragma unroll 4
-    for (int r = 0; r < P.ranges; ++r) v = add4(v, __ldg(reinterpret_cast<const float4*>(P.part_w) + r * n4 + i));
-    reinterpret_cast<float4*>(P.gW)[i] = v;
-  } else if (blk < P.gw + P.gg) {
+#pragma unroll 8
+    for (int64_t r = 0; r < rows; ++r) v = add4(v, __ldg(reinterpret_cast<const float4*>(part) + r * n4 + i));
+    return v;
+  };
+  auto together = [&](const float* part, int rows, int64_t n4, int64_t block, float* out) {
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-    const int n4 = P.d / 4;
-    const int64_t i = (blk - P.gw) * 32 + lane;
+    const int64_t i = block * 32 + lane;
     float4 v = zero;
     if (i < n4)
 #pragma unroll 4
-      for (int r = g; r < P.gain_rows; r += 8)
-        v = add4(v, __ldg(reinterpret_cast<const float4*>(P.part_gain) + static_cast<int64_t>(r) * n4 + i));
+      for (int r = g; r < rows; r += 8) v = add4(v, __ldg(reinterpret_cast<const float4*>(part) + r * n4 + i));
     red[g][lane] = v;
     __syncthreads();
     if (g != 0 || i >= n4) return;
     v = zero;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v = add4(v, red[k][lane]);
-    reinterpret_cast<float4*>(P.ggain)[i] = v;
+    reinterpret_cast<float4*>(out)[i] = v;
+  };
+  if (blk < P.gw) {
+    const int64_t n4 = static_cast<int64_t>(MIXN) * P.d, i = blk * 256 + threadIdx.x;
+    if (!P.few) together(P.part_w, P.ranges, n4, blk, P.gW);
+    else if (i < n4) reinterpret_cast<float4*>(P.gW)[i] = alone(P.part_w, P.ranges, n4, i);
+  } else if (blk < P.gw + P.gg) {
+    together(P.part_gain, P.gain_rows, P.d / 4, blk - P.gw, P.ggain);
   } else if (blk < P.gw + P.gg + P.gt) {
     const int64_t n4 = P.N * 5, i = (blk - P.gw - P.gg) * 256 + threadIdx.x;
     if (i >= n4) return;
-    float4 v = zero;
-#pragma unroll 8
-    for (int b = 0; b < P.col_blocks; ++b) v = add4(v, __ldg(reinterpret_cast<const float4*>(P.part_t) + b * n4 + i));
+    const float4 v = alone(P.part_t, P.col_blocks, n4, i);
     const int64_t t = i / 5;
     const int q = static_cast<int>(i - 5 * t);
     if (q == 0) reinterpret_cast<float4*>(P.gpost)[t] = v;
     else reinterpret_cast<float4*>(P.gcomb)[t * 4 + q - 1] = v;
   } else {
-    float* f = reinterpret_cast<float*>(red);
+    double* f = reinterpret_cast<double*>(red);
     const int j = threadIdx.x & 31, q = threadIdx.x >> 5;
-    float v = 0.f;
+    double sum = 0.0;
     if (j < MIXN + 3)
-      for (int b = q; b < P.mix_blocks; b += 8) v += __ldg(P.part_mix + static_cast<int64_t>(b) * 32 + j);
-    f[q * 32 + j] = v;
+      for (int b = q; b < P.mix_blocks; b += 8) sum += __ldg(P.part_mix + static_cast<int64_t>(b) * 32 + j);
+    f[q * 32 + j] = sum;
     __syncthreads();
     if (threadIdx.x >= MIXN + 3) return;
-    v = 0.f;
+    sum = 0.0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v += f[k * 32 + threadIdx.x];
+    for (int k = 0; k < 8; ++k) sum += f[k * 32 + threadIdx.x];
+    const float v = static_cast<float>(sum);
     if (threadIdx.x < MIXN) P.gbase[threadIdx.x] = v;
     else P.gscale[threadIdx.x - MIXN] = v;
   }
@@ -1016,10 +1039,8 @@ Plan search_plan(int64_t N, int d, int sms) {
     const int64_t nblocks = (d / 32 + spb - 1) / spb;
     for (int tt = SBR; tt >= 16; tt -= 16) {
       const int64_t tiles = (N + tt - 1) / tt;
-      const int64_t most = std::min<int64_t>(tiles, 64);
-      for (int64_t want = 1; want <= most; ++want) {
-        const int64_t per = (tiles + want - 1) / want, ranges = (tiles + per - 1) / per;
-        const int64_t rounds = (nblocks * ranges + sms - 1) / sms;
+      for (int64_t per = 1; per <= std::min<int64_t>(tiles, SB_RANGE); ++per) {
+        const int64_t ranges = (tiles + per - 1) / per, rounds = (nblocks * ranges + sms - 1) / sms;
         const int64_t cost = rounds * (per * (std::min(spb, d / 32) * (tt + 160) + 160) + 128);
         if (cost < best) {
           best = cost;
@@ -1187,7 +1208,8 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
   R.gain_rows = 3 * p.ranges;
   R.mix_blocks = p.mix_blocks;
   R.col_blocks = p.nblocks;
-  R.gw = (MIXN * d + 255) / 256;
+  R.few = p.ranges < 8;
+  R.gw = R.few ? (MIXN * d + 255) / 256 : (MIXN * d + 31) / 32;
   R.gg = (d / 4 + 31) / 32;
   R.gt = (N * 5 + 255) / 256;
   ckb_reduce_kernel<<<static_cast<unsigned>(R.gw + R.gg + R.gt + 1), 256, 0, stream>>>(R);

@@ -14,6 +14,18 @@
 //   q = sum_k u_k G_k (the gradient of Z),  S = sum h q F,  gF = r_F h q - (r_F^3 S / d) F,
 //   ggate = s gpost F r_F q (times a (1 - a) for the sigmoid),
 //   ggpost += s a F r_F q,  ggpre += gy yh r_y  over the tokens.
+//
+// A token depends on no other but through the gains' gradients, and its sums need whole rows before anything
+// is written. Three forms of each direction do that, chosen by the row's width:
+//   one warp a token (norm_step_rows, norm_step_backward_rows) for narrow rows: no barriers;
+//   the staged kernels (norm_step_staged, norm_step_backward_staged): a block a token, its rows copied to
+//     shared memory ahead, so that HBM is read once and the second look at a row costs nothing there;
+//   one block a token from global memory (norm_step_kernel, norm_step_backward_kernel) for rows of which
+//     shared memory does not hold a token.
+// Forward, 32,768 tokens of 4 x 5,120 with post norm and gate, 3.7 GB: 567 us, 96% of a plain copy's rate
+// (the form without staging 1,366 us). Backward, 16,384 tokens, 2.85 GB: 706 us, 60% of it: 11 warps of 164
+// registers a multiprocessor, which issue in 45% of the cycles (FMA pipe 28%); without staging 1,790 us.
+// One token of 4 x 5,120 forward: 6 us from C, nearly all of it the launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
