@@ -26,7 +26,7 @@
 //
 // Measured at 9,728 x 5,120: prep 23 us, token 171 us (0.74 GB, 4.3 TB/s, FMA pipe 59% busy), stream 358 us
 // (1.68 GB, 4.7 TB/s, FMA 38%, tensor 18%), reduce 12 us; the call at 32,768 x 5,120 1,830 us, at
-// 1,333 x 2,560 68 us, at 8 x 5,120 43 us (four kernels one after the other, 20 Sinkhorn rounds there and back
+// 1,333 x 2,560 68 us, at 8 x 5,120 36 us (four kernels one after the other, 20 Sinkhorn rounds there and back
 // in the first).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -951,7 +951,8 @@ struct ReduceParams {
   int ranges, gain_rows, mix_blocks, col_blocks;
   int gw, gg;
   int64_t gt;
-  bool few;   // ranges: fewer than a block's warps
+  bool few;          // ranges: fewer than a block's warps
+  bool few_tokens;   // 8 threads a sum of theirs fit the device at once
 };
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
@@ -967,7 +968,7 @@ __global__ void __launch_bounds__(256) ckb_reduce_kernel(const ReduceParams P) {
     for (int64_t r = 0; r < rows; ++r) v = add4(v, __ldg(reinterpret_cast<const float4*>(part) + r * n4 + i));
     return v;
   };
-  auto together = [&](const float* part, int rows, int64_t n4, int64_t block, float* out) {
+  auto together = [&](const float* part, int rows, int64_t n4, int64_t block, auto put) {
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t i = block * 32 + lane;
     float4 v = zero;
@@ -980,22 +981,25 @@ __global__ void __launch_bounds__(256) ckb_reduce_kernel(const ReduceParams P) {
     v = zero;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v = add4(v, red[k][lane]);
-    reinterpret_cast<float4*>(out)[i] = v;
+    put(i, v);
   };
-  if (blk < P.gw) {
-    const int64_t n4 = static_cast<int64_t>(MIXN) * P.d, i = blk * 256 + threadIdx.x;
-    if (!P.few) together(P.part_w, P.ranges, n4, blk, P.gW);
-    else if (i < n4) reinterpret_cast<float4*>(P.gW)[i] = alone(P.part_w, P.ranges, n4, i);
-  } else if (blk < P.gw + P.gg) {
-    together(P.part_gain, P.gain_rows, P.d / 4, blk - P.gw, P.ggain);
-  } else if (blk < P.gw + P.gg + P.gt) {
-    const int64_t n4 = P.N * 5, i = (blk - P.gw - P.gg) * 256 + threadIdx.x;
-    if (i >= n4) return;
-    const float4 v = alone(P.part_t, P.col_blocks, n4, i);
+  auto put_t = [&](int64_t i, float4 v) {   // gu, then the rows of gC, of a token
     const int64_t t = i / 5;
     const int q = static_cast<int>(i - 5 * t);
     if (q == 0) reinterpret_cast<float4*>(P.gpost)[t] = v;
     else reinterpret_cast<float4*>(P.gcomb)[t * 4 + q - 1] = v;
+  };
+  if (blk < P.gw) {
+    const int64_t n4 = static_cast<int64_t>(MIXN) * P.d, i = blk * 256 + threadIdx.x;
+    if (!P.few) together(P.part_w, P.ranges, n4, blk, [&](int64_t k, float4 v) { reinterpret_cast<float4*>(P.gW)[k] = v; });
+    else if (i < n4) reinterpret_cast<float4*>(P.gW)[i] = alone(P.part_w, P.ranges, n4, i);
+  } else if (blk < P.gw + P.gg) {
+    together(P.part_gain, P.gain_rows, P.d / 4, blk - P.gw,
+             [&](int64_t k, float4 v) { reinterpret_cast<float4*>(P.ggain)[k] = v; });
+  } else if (blk < P.gw + P.gg + P.gt) {
+    const int64_t n4 = P.N * 5, block = blk - P.gw - P.gg, i = block * 256 + threadIdx.x;
+    if (P.few_tokens) together(P.part_t, P.col_blocks, n4, block, put_t);
+    else if (i < n4) put_t(i, alone(P.part_t, P.col_blocks, n4, i));
   } else {
     double* f = reinterpret_cast<double*>(red);
     const int j = threadIdx.x & 31, q = threadIdx.x >> 5;
@@ -1211,7 +1215,9 @@ cudaError_t launch_backward_ckpt(const BwdArgs& a, const BwdCheckpoint& ck, cuda
   R.few = p.ranges < 8;
   R.gw = R.few ? (MIXN * d + 255) / 256 : (MIXN * d + 31) / 32;
   R.gg = (d / 4 + 31) / 32;
-  R.gt = (N * 5 + 255) / 256;
+  // (one thread a sum took 17 us in all for 8 x 5,120, whose 80 column blocks it walks alone)
+  R.few_tokens = N * 5 * 8 <= 2048 * static_cast<int64_t>(sms);
+  R.gt = R.few_tokens ? (N * 5 + 31) / 32 : (N * 5 + 255) / 256;
   ckb_reduce_kernel<<<static_cast<unsigned>(R.gw + R.gg + R.gt + 1), 256, 0, stream>>>(R);
   return cudaGetLastError();
 }
