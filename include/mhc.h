@@ -247,7 +247,7 @@ size_t mhc_checkpoint_scale_bytes(int64_t rows, int d);
  * X'. The decoded values stand in for X and F, X' = hc_post of them in the forward's float32
  * arithmetic, rounded to bf16, y_hat = hc_pre(X') rounded to bf16; mixes is the forward's m, whose
  * gradient g_m is that of the forward. All else as there, but in four kernels, with r g_m and W held
- * to float32's accuracy in three bf16 planes each.
+ * to float32's accuracy in three bf16 planes each, and sinkhorn_iters at most 4096 (MHC_ERR_SHAPE).
  * workspace: >= mhc_backward_ckpt_workspace_bytes(N, n, d) device bytes, 16-byte aligned.      */
 int mhc_fused_step_backward_ckpt(const void* X_codes, const void* X_scale, const void* F_codes,
                                  const void* F_scale, const float* mixes, const float* pre_prev,

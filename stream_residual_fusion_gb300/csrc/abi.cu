@@ -221,13 +221,17 @@ int fused_common(const void* X, const void* F, const float* pre_prev, const floa
   return cuda_code(launch_step(true, a, s));
 }
 
+// Rounds of Sinkhorn that the backward from checkpoints takes: its time grows with their square where they
+// are more than the steps whose inputs it keeps (4,096 rounds: seconds at most).
+constexpr int kMaxCkptIters = 4096;
+
 // Checks and launch shared by the two backward entries: from X, F and X', or (`c` set) from
 // checkpoints of X and F.
 int backward_common(const BwdArgs& a, int n, const BwdCheckpoint* c, void* stream) {
   const int64_t N = a.N;
   const int d = a.d;
   if (n != 4 || N < 0 || N > kMaxTokens || d <= 0 || d % 64 != 0 || a.iters < 1) return MHC_ERR_SHAPE;
-  if ((a.flags & ~MHC_COMB_ROW_DEST) != 0) return MHC_ERR_SHAPE;
+  if ((a.flags & ~MHC_COMB_ROW_DEST) != 0 || (c && a.iters > kMaxCkptIters)) return MHC_ERR_SHAPE;
   if (!a.W || !a.scale || !a.base || !a.gain || !a.gW || !a.gbase || !a.gscale || !a.ggain) return MHC_ERR_NULL;
   const void* params[] = {a.W, a.scale, a.base, a.gain, a.gW, a.gbase, a.gscale, a.ggain};
   for (const void* p : params)

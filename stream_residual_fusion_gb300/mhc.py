@@ -488,7 +488,7 @@ def _norm_step_backward(call, where, saved, N, n, d, gXp, gy, gain_post, gain_pr
         likes["ggain_post"] = gain_post
     if gate is not None:
         likes["ggate"] = gate
-    if pre is not None:
+    if pre is not None and post is not None and comb is not None:   # (some of them: refused below)
         likes.update(gpre=pre, gpost=post, gcomb=comb)
     o = _made(out, likes, device, stream)
     if workspace is None:

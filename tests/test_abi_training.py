@@ -50,7 +50,7 @@ def _bwd(M, N=256, n=4, d=5120, iters=20, flags=0, ptrs=None, ws=None, ws_bytes=
 
 
 def test_step_backward_ckpt_validation(M):
-    for kw in (dict(n=1), dict(N=-1), dict(iters=0), dict(d=5120 + 32), dict(flags=0x2)):
+    for kw in (dict(n=1), dict(N=-1), dict(iters=0), dict(iters=4097), dict(d=5120 + 32), dict(flags=0x2)):
         assert _bwd(M, **kw) == M.MHC_ERR_SHAPE, kw
     for i in range(26):
         p = [_addr(k) for k in range(26)]

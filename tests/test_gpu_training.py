@@ -407,6 +407,21 @@ def test_norm_step_bounds_empty_and_refusals(M):
         M.norm_step_backward(a["X"], a["F"], a["gXp"], a["gy"], *pos, **kw,
                              workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     assert err.value.code == M.MHC_ERR_WORKSPACE
+    for some in (dict(post=None), dict(pre=None), dict(pre=None, comb=None)):   # weights: all or none
+        with pytest.raises(M.MhcError):
+            M.norm_step(a["X"], a["F"], *pos, **dict(kw, **some))
+        with pytest.raises(M.MhcError):
+            M.norm_step_backward(a["X"], a["F"], a["gXp"], a["gy"], *pos, **dict(kw, **some))
+
+
+@pytest.mark.parametrize("N,n,d", [(70, 1, 72), (700, 4, 64), (331, 1, 1992), (309, 4, 1032), (3, 4, 32768)])
+def test_norm_step_in_place(M, N, n, d):
+    a = _norm_inputs(N, n, d, "sigmoid", True, True, False, 8)
+    kw, _ = _norm_kw(M, a, "sigmoid", False, False, 0.5, 1e-6)
+    want = M.norm_step(a["X"], a["F"], a["gain_post"], a["gain_pre"], **kw)
+    X = a["X"].clone()
+    got = M.norm_step(X, a["F"], a["gain_post"], a["gain_pre"], **kw, out={"Xp": X})
+    assert got["Xp"] is X and torch.equal(X, want["Xp"]) and torch.equal(got["y"], want["y"])
 
 
 @pytest.mark.parametrize("n,shared", [(1, False), (4, True)])
