@@ -819,42 +819,39 @@ __device__ __forceinline__ void pass_sums(const NormArgs& P, const Rows& R, cons
     }
   }
 }
+template <int NS>
+__device__ __forceinline__ float pick(const float (&a)[NS], int i) {
+  float v = a[0];
+#pragma unroll
+  for (int k = 1; k < NS; ++k) v = i == k ? a[k] : v;
+  return v;
+}
 // The weights' gradients of token t by one warp, lane l of which has the sum l: written, or with shared weights
-// added to this lane's gp and to its gu or gC.
+// added to this lane's gp and to its gu or gC. Each lane has one of them to finish and to store: with a test
+// and a store for each of the 24 the other warps waited for this one (880 us against 706 with shared weights,
+// at 16,384 x 4 x 5,120).
 template <int NS, bool CK>
 __device__ __forceinline__ void weight_gradients(const NormArgs& P, int64_t t, const Weights<NS>& w, float tot,
                                                  float ry, float tau, float& total_gp, float& total_w) {
   using S = Sums<NS, CK>;
   const int lane = threadIdx.x & 31;
-  const bool shared = (P.flags & FLAG_WEIGHTS_SHARED) != 0, row_dest = (P.flags & 1u) != 0;
   const float e = ry * tot - tau * __shfl_down_sync(0xffffffffu, tot, NS + 1);   // lanes E ..: e_z, e_j
-  const float ez = lane_value(e, S::E);
-  float ej[NS];
+  // gp_k in lanes 0 .. NS - 1
+  float gp = pick<NS>(w.u, lane) * lane_value(e, S::E);
 #pragma unroll
-  for (int j = 0; j < NS; ++j) ej[j] = lane_value(e, S::E + 1 + j);
-#pragma unroll
-  for (int k = 0; k < NS; ++k) {
-    float gp = w.u[k] * ez;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) gp = fmaf(w.cc[j][k], ej[j], gp);
-    if (lane == k) {
-      if (shared) total_gp += gp;
-      else P.gpre[t * NS + k] = gp;
-    }
-    if (lane == S::G + k) {
-      const float gu = fmaf(w.p[k], ez, tot);
-      if (shared) total_w += gu;
-      else P.gpost[t * NS + k] = gu;
-    }
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      if (lane == S::G + NS + j * NS + k) {
-        const float gc = fmaf(w.p[k], ej[j], tot);
-        if (shared) total_w += gc;
-        else P.gcomb[t * NS * NS + (row_dest ? k * NS + j : j * NS + k)] = gc;
-      }
-    }
+  for (int j = 0; j < NS; ++j) gp = fmaf(pick<NS>(w.cc[j], lane), lane_value(e, S::E + 1 + j), gp);
+  // lanes G ..: gu_k with e_z, then gC_jk with e_j
+  const int i = max(lane - S::G, 0), k = i & (NS - 1);
+  const float g = fmaf(pick<NS>(w.p, k), __shfl_sync(0xffffffffu, e, S::E + i / NS), tot);
+  const bool late = lane >= S::G && lane < S::V;
+  if (P.flags & FLAG_WEIGHTS_SHARED) {
+    if (lane < NS) total_gp += gp;
+    if (late) total_w += g;
+    return;
   }
+  if (lane < NS) P.gpre[t * NS + lane] = gp;
+  const int jk = (P.flags & 1u) != 0 ? k * NS + (i / NS - 1) : i - NS;
+  if (late) (i < NS ? P.gpost + t * NS : P.gcomb + t * NS * NS)[i < NS ? i : jk] = g;
 }
 // The second pass: gX and ggate, the gains' sums, and this thread's part of S; leaves h q in place of yh.
 template <int NS, bool CK, int UN>
