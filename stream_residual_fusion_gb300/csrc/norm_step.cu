@@ -935,7 +935,7 @@ __device__ __forceinline__ void put_gains(float* row, int d, const Span4& sp, co
 
 // Threads of the backward's blocks: 11 consumer warps and the producer, at 168 registers a thread. BOUND caps the
 // registers further where that lets a multiprocessor hold more blocks of few threads: 512 for 128 registers,
-// 768 for 80.
+// 640 for 96, 768 for 80.
 constexpr int SBACK_THREADS = 384;
 
 template <int NS, bool CK, int UN, int BOUND = SBACK_THREADS>
@@ -1258,24 +1258,30 @@ int staged_threads(int items, int each, int most) {
 // Shared memory left free for the L1 cache where that can be: the gains, read for every token.
 int l1_room(int d) { return 12 * d; }
 
+constexpr int kStatic = 4096;   // the staged kernels' static shared memory and the system's share of it, at most
+
+// Blocks of a staged kernel that a multiprocessor holds with two stages each, at most `cap`; at least 1.
+int staged_blocks(const void* kernel, int threads, const Stage& S, const DeviceInfo& dev, int d, int cap) {
+  const int one = S.bytes + S.xbytes, room = dev.smem - kStatic, block = threads + 32;
+  const int per = std::max(1, std::min({cap, (room - l1_room(d)) / (2 * one + kStatic), 2048 / block}));
+  if (per == 1) return 1;
+  // warps a multiprocessor's four register files hold, 16,384 registers each
+  const int held = 4 * (16384 / (32 * ((kernel_registers(kernel) + 7) / 8 * 8)));
+  return std::max(1, std::min(per, held / (block / 32)));
+}
+
 // Launches a staged kernel (`kernel`, its stage sizes S) where a stage fits at all. cap: blocks per
 // multiprocessor. *ran: the launched blocks, 0 if the kernel does not take this size.
 template <typename K>
 cudaError_t launch_staged(K kernel, const NormArgs& a, int threads, const Stage& S, const DeviceInfo& dev, int cap,
                           int* ran, cudaStream_t stream) {
   *ran = 0;
-  constexpr int kStatic = 4096;   // the kernels' static shared memory and the system's share of it, at most
   const int one = S.bytes + S.xbytes, room = dev.smem - kStatic;
   if (threads == 0 || one > room) return cudaSuccess;
   // several blocks a multiprocessor where two stages of each fit, else one block with two stages of the
   // rows and one of X, else one of each
   const int block = threads + 32;
-  int per = std::max(1, std::min({cap, (room - l1_room(a.d)) / (2 * one + kStatic), 2048 / block}));
-  if (per > 1) {
-    // warps a multiprocessor's four register files hold, 16,384 registers each
-    const int held = 4 * (16384 / (32 * ((kernel_registers(reinterpret_cast<const void*>(kernel)) + 7) / 8 * 8)));
-    per = std::max(1, std::min(per, held / (block / 32)));
-  }
+  const int per = staged_blocks(reinterpret_cast<const void*>(kernel), threads, S, dev, a.d, cap);
   Ring R{1, 1};
   const int space = room / per - (per > 1 ? kStatic : 0) - l1_room(a.d) / per;
   if (2 * one <= space) {
@@ -1347,21 +1353,36 @@ cudaError_t backward_of(const NormArgs& a, const DeviceInfo& dev, int* rows, cud
     auto run = [&](auto kernel, int threads) {
       return launch_staged(kernel, a, threads, stage, dev, NORM_BACK_BLOCKS, rows, stream);
     };
-    // Two units a thread where that fits (four streams, 128 registers: 301 us at 20,480 x 4 x 1,024, 398 with
-    // 168). At middling widths more units make blocks of fewer threads, more of which fit: four units of one
-    // stream (389 us against 455 at 40,960 x 2,048), three of four streams (300 against 418 at 10,240 x 4 x 2,048).
+    // Two units a thread where that fits. Four streams: 128 registers (301 us at 20,480 x 4 x 1,024, 398 with 168;
+    // from checkpoints 128 spill). One stream: 96, from checkpoints (80 spill: 430 us against 331 at 65,536 x 1,024)
+    // and where as many blocks fit as with 80 (297 against 314 there without checkpoints), else 80 for two blocks
+    // of wider rows (218 against 269 at 16,384 x 2,688).
+    auto two = [&]() {
+      if constexpr (NS == 4) return run(norm_step_backward_staged<NS, CK, 2, CK ? SBACK_THREADS : 512>, t2);
+      else if constexpr (CK) return run(norm_step_backward_staged<NS, CK, 2, 640>, t2);
+      else return t2 <= 128 ? run(norm_step_backward_staged<NS, CK, 2, 640>, t2)
+                            : run(norm_step_backward_staged<NS, CK, 2, 768>, t2);
+    };
+    // More units make smaller blocks. Four streams: three units where so many more blocks fit that a multiprocessor
+    // holds more consumers (245 us against 267 at 20,480 x 4 x 1,280, 213 against 236 at 10,240 x 4 x 2,048; where
+    // not, two are faster, 166 against 213 at 10,240 x 4 x 1,536). One stream: four units at middling widths
+    // (326 against 399 at 40,960 x 2,048).
     auto middling = [&]() {
       if constexpr (NS == 1) {
         if (t4 >= 96 && t4 <= 160) return run(norm_step_backward_staged<NS, CK, 4, 512>, t4);
       } else if constexpr (!CK) {
         const int t3 = staged_threads(a.d / 4, 3, most);
-        if (t3 >= 128 && t3 <= 192) return run(norm_step_backward_staged<NS, CK, 3, 512>, t3);
+        auto held = [&](auto kernel, int threads) {
+          return threads * staged_blocks(reinterpret_cast<const void*>(kernel), threads, stage, dev, a.d, NORM_BACK_BLOCKS);
+        };
+        if (t2 > 0 && held(norm_step_backward_staged<NS, CK, 3, 512>, t3) > held(norm_step_backward_staged<NS, CK, 2, 512>, t2))
+          return run(norm_step_backward_staged<NS, CK, 3, 512>, t3);
       }
       return cudaSuccess;
     };
     cudaError_t e = middling();
     if (e != cudaSuccess || *rows > 0) return e;
-    if (t2 > 0) e = run(norm_step_backward_staged<NS, CK, 2, NS == 1 ? 768 : CK ? SBACK_THREADS : 512>, t2);
+    if (t2 > 0) e = two();
     else if (t4 > 0) e = run(norm_step_backward_staged<NS, CK, 4>, t4);
     else e = run(norm_step_backward_staged<NS, CK, 6>, staged_threads(a.d / 4, 6, most));
     if (e != cudaSuccess || *rows > 0) return e;
