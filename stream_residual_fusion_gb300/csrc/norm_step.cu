@@ -23,8 +23,8 @@
 //   one block a token from global memory (norm_step_kernel, norm_step_backward_kernel) for rows of which
 //     shared memory does not hold a token.
 // Forward, 32,768 tokens of 4 x 5,120 with post norm and gate, 3.7 GB: 567 us, 96% of a plain copy's rate
-// (the form without staging 1,366 us). Backward, 16,384 tokens, 2.85 GB: 706 us, 60% of it: 11 warps of 164
-// registers a multiprocessor, which issue in 45% of the cycles (FMA pipe 28%); without staging 1,790 us.
+// (the form without staging 1,366 us). Backward, 16,384 tokens, 2.85 GB: 668 us, 63% of it: 11 warps of 164
+// registers a multiprocessor, which issue in 46% of the cycles (FMA pipe 30%); without staging 1,790 us.
 // One token of 4 x 5,120 forward: 6 us from C, nearly all of it the launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
