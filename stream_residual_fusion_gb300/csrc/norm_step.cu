@@ -362,13 +362,21 @@ template <int NS, bool CK, bool BACK>
 __host__ __device__ constexpr Stage stage_of(int d) {
   Stage s{};
   const int e = CK ? 1 : 2;
-  s.gate = d * e;
+  s.gate = CK ? (d + 15) / 16 * 16 : 2 * d;
   s.gxp = s.gate + 2 * d;
   s.gy = s.gxp + (BACK ? NS * 2 * d : 0);
   s.w = s.gy + (BACK ? 2 * d : 0);
   s.bytes = (s.w + (NS == 4 ? 96 : 0) + 127) / 128 * 128;
-  s.xbytes = (NS * d * e + 127) / 128 * 128;
+  s.xbytes = (NS * d * e + (CK && NS == 1 ? 8 : 0) + 127) / 128 * 128;
   return s;
+}
+// Bulk copies take whole 16-byte units. Where a row of codes has 8 bytes more, every second one begins in the
+// middle of a unit: such rows are copied with the 8 bytes before or behind them, so that row t lies this far into
+// its place. (The four streams of a token always make whole units.) 20,480 x 4 x 1,000 from checkpoints: 238 us,
+// straight from global memory 1,286.
+template <bool CK>
+__device__ __forceinline__ int row_start(int64_t t, int d) {
+  return CK ? 8 * static_cast<int>(t & (d >> 3) & 1) : 0;
 }
 // Stages of a block: of a token's rows, and of its X.
 struct Ring {
@@ -442,12 +450,28 @@ __device__ __forceinline__ bool produce(const NormArgs& P, uint8_t* sm, Barriers
   const Stage S = stage_of<NS, CK, BACK>(P.d);
   const uint64_t pol = policy_evict_first();
   const uint32_t row = 2u * P.d, saved = (CK ? 1u : 2u) * P.d;
-  const uint32_t bytes = saved + (P.gate ? row : 0u) + (BACK ? (NS + 1) * row : 0u) + (NS == 4 ? 96u : 0u);
+  const uint32_t bytes = (P.gate ? row : 0u) + (BACK ? (NS + 1) * row : 0u) + (NS == 4 ? 96u : 0u);   // but F's
   uint8_t* xs = sm + R.rows * S.bytes;
   bool late = false;
   // the first use of a stage waits for nobody, a later one for the release of the use before it
   auto free_of = [&](uint64_t* empty, const Place& p, bool used) {
     if (used && !mbar_wait(&empty[p.stage], p.parity ^ 1u, late ? 0ull : NORM_WAIT_NS)) late = true;
+  };
+  // Row t of `base` to dst. The last row has nothing behind it: 8 bytes of it are copied here.
+  auto load_row = [&](uint8_t* dst, const void* base, int64_t t, uint64_t* full, uint32_t more) {
+    const uint8_t* src = static_cast<const uint8_t*>(base) + t * saved;
+    uint32_t n = saved;
+    if (CK && (saved & 8u) != 0) {
+      const int before = row_start<CK>(t, P.d);
+      src -= before;
+      n += 8;
+      if (before == 0 && t + 1 == P.N) {
+        n -= 16;
+        *reinterpret_cast<uint2*>(dst + n) = __ldg(reinterpret_cast<const uint2*>(src + n));
+      }
+    }
+    mbar_arrive_expect_tx(full, n + more);
+    bulk_load_hint(dst, src, n, full, pol);
   };
   Place rp, xp;
   bool rused = false, xused = false;
@@ -456,8 +480,7 @@ __device__ __forceinline__ bool produce(const NormArgs& P, uint8_t* sm, Barriers
     auto at = [&](const void* p, int64_t n) { return static_cast<const uint8_t*>(p) + t * n; };
     free_of(B.empty, rp, rused);
     uint8_t* st = sm + b * S.bytes;
-    mbar_arrive_expect_tx(&B.full[b], bytes);
-    bulk_load_hint(st, at(P.F, saved), saved, &B.full[b], pol);
+    load_row(st, P.F, t, &B.full[b], bytes);
     if (P.gate) bulk_load_hint(st + S.gate, at(P.gate, row), row, &B.full[b], pol);
     if (BACK) {
       bulk_load_hint(st + S.gy, at(P.gy, row), row, &B.full[b], pol);
@@ -470,8 +493,12 @@ __device__ __forceinline__ bool produce(const NormArgs& P, uint8_t* sm, Barriers
       bulk_load_hint(st + S.w + 32, P.comb + wt * 16, 64, &B.full[b], pol);
     }
     free_of(B.xempty, xp, xused);
-    mbar_arrive_expect_tx(&B.xfull[x], NS * saved);
-    bulk_load_hint(xs + x * S.xbytes, at(P.X, static_cast<int64_t>(NS) * saved), NS * saved, &B.xfull[x], pol);
+    if (NS == 1) {
+      load_row(xs + x * S.xbytes, P.X, t, &B.xfull[x], 0u);
+    } else {
+      mbar_arrive_expect_tx(&B.xfull[x], NS * saved);
+      bulk_load_hint(xs + x * S.xbytes, at(P.X, static_cast<int64_t>(NS) * saved), NS * saved, &B.xfull[x], pol);
+    }
     rp.next(R.rows);
     xp.next(R.x);
     rused |= rp.stage == 0;
@@ -974,10 +1001,13 @@ __global__ void __launch_bounds__(BOUND, 1)
     for (int64_t t = blockIdx.x; t < P.N; t += gridDim.x, ++n) {
       const int stage = rp.stage;
       const uint8_t* st = sm + stage * G.bytes;
-      const Rows rows{st, st + G.gate, st + G.gxp, st + G.gy, sm + R.rows * G.bytes + xp.stage * G.xbytes};
+      const int in = row_start<CK>(t, P.d);
+      const uint8_t* fr = st + in;
+      const Rows rows{fr, st + G.gate, st + G.gxp, st + G.gy,
+                      sm + R.rows * G.bytes + xp.stage * G.xbytes + (NS == 1 ? in : 0)};
       wait(B.full, rp);
       if (P.gain_post && (n == 0 || !ahead)) {
-        float v[1] = {sum_f2<CK, UN>(st, sp, sc)};
+        float v[1] = {sum_f2<CK, UN>(fr, sp, sc)};
         r = inv_rms(group_sums<1>(v, scratch1, warps, T), inv_d, P.eps);
       }
       scale_codes<NS, CK, UN>(P, t + gridDim.x, sp, sn);
@@ -1030,11 +1060,11 @@ __global__ void __launch_bounds__(BOUND, 1)
       rp.next(R.rows);
       if (P.gain_post && ahead && t + gridDim.x < P.N) {
         wait(B.full, rp);
-        v[1] = sum_f2<CK, UN>(sm + rp.stage * G.bytes, sp, sn);
+        v[1] = sum_f2<CK, UN>(sm + rp.stage * G.bytes + row_start<CK>(t + gridDim.x, P.d), sp, sn);
       }
       const float tot3 = P.gain_post ? group_sums<2>(v, scratch3, warps, T) : 0.f;
       const float cf = P.gain_post ? r * r * r * lane_value(tot3, 0) * inv_d : 0.f;
-      write_gf<CK, UN>(P, t, st, sp, sc, r, cf, yh);
+      write_gf<CK, UN>(P, t, fr, sp, sc, r, cf, yh);
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.empty[stage]);
       if (P.gain_post) r = inv_rms(lane_value(tot3, 1), inv_d, P.eps);
@@ -1339,54 +1369,52 @@ template <int NS, bool CK>
 cudaError_t backward_of(const NormArgs& a, const DeviceInfo& dev, int* rows, cudaStream_t stream) {
   *rows = 0;
   const int lanes = (a.d / 4 + 31) / 32;   // units a lane, one warp a token
-  if (lanes <= 4) {
+  // (four streams of 512 features: 277 us against 231 a block a token from checkpoints, 244 against 231 without)
+  if (lanes <= (NS == 4 ? 3 : 4)) {
     *rows = warp_blocks(a.N, dev, NS == 4 ? 3 : 4);
     return lanes <= 1 ? launch_warps(norm_step_backward_rows<NS, CK, 1>, a, *rows, stream)
            : lanes <= 2 ? launch_warps(norm_step_backward_rows<NS, CK, 2>, a, *rows, stream)
                         : launch_warps(norm_step_backward_rows<NS, CK, 4>, a, *rows, stream);
   }
-  // bulk copies of a row of codes take whole 16-byte units
-  if (!CK || a.d % 16 == 0) {
-    const Stage stage = stage_of<NS, CK, true>(a.d);
-    const int most = SBACK_THREADS - 32;
-    const int t2 = staged_threads(a.d / 4, 2, most), t4 = staged_threads(a.d / 4, 4, most);
-    auto run = [&](auto kernel, int threads) {
-      return launch_staged(kernel, a, threads, stage, dev, NORM_BACK_BLOCKS, rows, stream);
-    };
-    // Two units a thread where that fits. Four streams: 128 registers (301 us at 20,480 x 4 x 1,024, 398 with 168;
-    // from checkpoints 128 spill). One stream: 96, from checkpoints (80 spill: 430 us against 331 at 65,536 x 1,024)
-    // and where as many blocks fit as with 80 (297 against 314 there without checkpoints), else 80 for two blocks
-    // of wider rows (218 against 269 at 16,384 x 2,688).
-    auto two = [&]() {
-      if constexpr (NS == 4) return run(norm_step_backward_staged<NS, CK, 2, CK ? SBACK_THREADS : 512>, t2);
-      else if constexpr (CK) return run(norm_step_backward_staged<NS, CK, 2, 640>, t2);
-      else return t2 <= 128 ? run(norm_step_backward_staged<NS, CK, 2, 640>, t2)
-                            : run(norm_step_backward_staged<NS, CK, 2, 768>, t2);
-    };
-    // More units make smaller blocks. Four streams: three units where so many more blocks fit that a multiprocessor
-    // holds more consumers (245 us against 267 at 20,480 x 4 x 1,280, 213 against 236 at 10,240 x 4 x 2,048; where
-    // not, two are faster, 166 against 213 at 10,240 x 4 x 1,536). One stream: four units at middling widths
-    // (326 against 399 at 40,960 x 2,048).
-    auto middling = [&]() {
-      if constexpr (NS == 1) {
-        if (t4 >= 96 && t4 <= 160) return run(norm_step_backward_staged<NS, CK, 4, 512>, t4);
-      } else if constexpr (!CK) {
-        const int t3 = staged_threads(a.d / 4, 3, most);
-        auto held = [&](auto kernel, int threads) {
-          return threads * staged_blocks(reinterpret_cast<const void*>(kernel), threads, stage, dev, a.d, NORM_BACK_BLOCKS);
-        };
-        if (t2 > 0 && held(norm_step_backward_staged<NS, CK, 3, 512>, t3) > held(norm_step_backward_staged<NS, CK, 2, 512>, t2))
-          return run(norm_step_backward_staged<NS, CK, 3, 512>, t3);
-      }
-      return cudaSuccess;
-    };
-    cudaError_t e = middling();
-    if (e != cudaSuccess || *rows > 0) return e;
-    if (t2 > 0) e = two();
-    else if (t4 > 0) e = run(norm_step_backward_staged<NS, CK, 4>, t4);
-    else e = run(norm_step_backward_staged<NS, CK, 6>, staged_threads(a.d / 4, 6, most));
-    if (e != cudaSuccess || *rows > 0) return e;
-  }
+  const Stage stage = stage_of<NS, CK, true>(a.d);
+  const int most = SBACK_THREADS - 32;
+  const int t2 = staged_threads(a.d / 4, 2, most), t4 = staged_threads(a.d / 4, 4, most);
+  auto run = [&](auto kernel, int threads) {
+    return launch_staged(kernel, a, threads, stage, dev, NORM_BACK_BLOCKS, rows, stream);
+  };
+  // Two units a thread where that fits. Four streams: 128 registers (301 us at 20,480 x 4 x 1,024, 398 with 168;
+  // from checkpoints 128 spill). One stream: 96, from checkpoints (80 spill: 430 us against 331 at 65,536 x 1,024)
+  // and where as many blocks fit as with 80 (297 against 314 there without checkpoints), else 80 for two blocks
+  // of wider rows (218 against 269 at 16,384 x 2,688).
+  auto two = [&]() {
+    if constexpr (NS == 4) return run(norm_step_backward_staged<NS, CK, 2, CK ? SBACK_THREADS : 512>, t2);
+    else if constexpr (CK) return run(norm_step_backward_staged<NS, CK, 2, 640>, t2);
+    else return t2 <= 128 ? run(norm_step_backward_staged<NS, CK, 2, 640>, t2)
+                          : run(norm_step_backward_staged<NS, CK, 2, 768>, t2);
+  };
+  // More units make smaller blocks. Four streams: three units where so many more blocks fit that a multiprocessor
+  // holds more consumers (245 us against 267 at 20,480 x 4 x 1,280, 213 against 236 at 10,240 x 4 x 2,048; where
+  // not, two are faster, 166 against 213 at 10,240 x 4 x 1,536). One stream: four units at middling widths
+  // (326 against 399 at 40,960 x 2,048).
+  auto middling = [&]() {
+    if constexpr (NS == 1) {
+      if (t4 >= 96 && t4 <= 160) return run(norm_step_backward_staged<NS, CK, 4, 512>, t4);
+    } else if constexpr (!CK) {
+      const int t3 = staged_threads(a.d / 4, 3, most);
+      auto held = [&](auto kernel, int threads) {
+        return threads * staged_blocks(reinterpret_cast<const void*>(kernel), threads, stage, dev, a.d, NORM_BACK_BLOCKS);
+      };
+      if (t2 > 0 && held(norm_step_backward_staged<NS, CK, 3, 512>, t3) > held(norm_step_backward_staged<NS, CK, 2, 512>, t2))
+        return run(norm_step_backward_staged<NS, CK, 3, 512>, t3);
+    }
+    return cudaSuccess;
+  };
+  cudaError_t e = middling();
+  if (e != cudaSuccess || *rows > 0) return e;
+  if (t2 > 0) e = two();
+  else if (t4 > 0) e = run(norm_step_backward_staged<NS, CK, 4>, t4);
+  else e = run(norm_step_backward_staged<NS, CK, 6>, staged_threads(a.d / 4, 6, most));
+  if (e != cudaSuccess || *rows > 0) return e;
   *rows = static_cast<int>(std::min<int64_t>(a.N, 2 * static_cast<int64_t>(dev.sms)));
   return launch_rows(norm_step_backward_kernel<NS, CK>, a, *rows, stream);
 }

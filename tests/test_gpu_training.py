@@ -294,6 +294,11 @@ NORM_CASES = [
     (130, 1, 200, "linear", True, True, True, False),
     (600, 1, 1024, "sigmoid", False, False, False, False),
     (6, 4, 7168, "none", False, True, True, False),
+    (1, 1, 520, "linear", True, False, False, False),      # codes of 8 bytes beyond whole 16: one row, and more
+    (306, 1, 1000, "sigmoid", True, True, False, False),
+    (457, 4, 520, "linear", True, True, False, False),
+    (458, 4, 1000, "none", True, True, False, True),
+    (153, 1, 5128, "none", True, False, False, False),
 ]
 
 
