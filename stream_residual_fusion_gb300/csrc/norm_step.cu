@@ -1355,11 +1355,19 @@ cudaError_t forward_of(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st
   cudaError_t e;
   auto run = [&](auto kernel, int threads) { return launch_staged(kernel, a, threads, stage, dev, 8, &ran, stream); };
   const int t1 = staged_threads(a.d / 8, 1, most), t2 = staged_threads(a.d / 8, 2, most);
-  // one stream: two chunks a thread and 80 registers, for more and smaller blocks a multiprocessor
-  // (2,048 features: 203 -> 185 us at 40,960 tokens)
-  constexpr int kBound = NS == 1 ? 768 : (SMAX_WARPS + 1) * 32;
+  // One stream: two chunks a thread, and 96 registers (80 spill: 182 us against 161 at 40,000 x 2,048 with a sigmoid)
+  // unless 80 let many more blocks fit (188 against 221 at 16,384 x 5,120, 121 against 126 at 20,000 x 2,560).
+  auto two = [&]() {
+    if constexpr (NS == 1) {
+      auto fit = [&](auto kernel) { return staged_blocks(reinterpret_cast<const void*>(kernel), t2, stage, dev, a.d, 8); };
+      return 6 * fit(norm_step_staged<NS, 2, 640>) >= 5 * fit(norm_step_staged<NS, 2, 768>)
+                 ? run(norm_step_staged<NS, 2, 640>, t2) : run(norm_step_staged<NS, 2, 768>, t2);
+    } else {
+      return run(norm_step_staged<NS, 2>, t2);
+    }
+  };
   if (NS == 4 && t1 > 0) e = run(norm_step_staged<4, 1>, t1);
-  else if (t2 > 0) e = run(norm_step_staged<NS, 2, kBound>, t2);
+  else if (t2 > 0) e = two();
   else e = run(norm_step_staged<NS, 4>, staged_threads(a.d / 8, 4, most));
   if (e != cudaSuccess || ran > 0) return e;
   return launch_rows(norm_step_kernel<NS>, a, std::min<int64_t>(a.N, static_cast<int64_t>(dev.sms) * 8), stream);
