@@ -1402,11 +1402,12 @@ cudaError_t backward_of(const NormArgs& a, const DeviceInfo& dev, int* rows, cud
   };
   // More units make smaller blocks. Four streams: three units where so many more blocks fit that a multiprocessor
   // holds more consumers (245 us against 267 at 20,480 x 4 x 1,280, 213 against 236 at 10,240 x 4 x 2,048; where
-  // not, two are faster, 166 against 213 at 10,240 x 4 x 1,536). One stream: four units at middling widths
-  // (326 against 399 at 40,960 x 2,048).
+  // not, two are faster, 166 against 213 at 10,240 x 4 x 1,536). One stream: four units at middling widths, up
+  // to where two blocks of them fit (326 against 399 us at 40,960 x 2,048, 278 against 361 at 16,384 x 3,328); the
+  // widest that two units take are as fast with those from bf16 (258 against 267 at 16,384 x 2,816).
   auto middling = [&]() {
     if constexpr (NS == 1) {
-      if (t4 >= 96 && t4 <= 160) return run(norm_step_backward_staged<NS, CK, 4, 512>, t4);
+      if (t4 >= 96 && t4 <= (CK || t2 == 0 ? 224 : 160)) return run(norm_step_backward_staged<NS, CK, 4, 512>, t4);
     } else if constexpr (!CK) {
       const int t3 = staged_threads(a.d / 4, 3, most);
       auto held = [&](auto kernel, int threads) {

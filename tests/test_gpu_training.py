@@ -299,6 +299,10 @@ NORM_CASES = [
     (457, 4, 520, "linear", True, True, False, False),
     (458, 4, 1000, "none", True, True, False, True),
     (153, 1, 5128, "none", True, False, False, False),
+    (170, 1, 2688, "sigmoid", True, False, False, False),
+    (331, 1, 1160, "linear", False, True, False, False),
+    (155, 1, 7168, "sigmoid", True, True, True, False),
+    (160, 1, 3344, "none", True, False, False, False),
 ]
 
 
